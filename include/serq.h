@@ -487,7 +487,8 @@ const char* serq_last_error_string(void);
 serq_status serq_check_device(void);
 
 /* Reads and clears the device-side status word that kernels set when a
- * bounded wait gives up (0 = none).  Synchronises the current device. */
+ * bounded wait gives up (1-4) or a page table entry in use is invalid (5;
+ * 0 = none).  Synchronises the current device. */
 serq_status serq_device_error(int* code);
 
 /*
@@ -600,6 +601,169 @@ serq_status serq_mx_quantize_act(const void* Xh, serq_dtype dtype, int M, int K,
  */
 serq_status serq_mx_linear(const serq_mx_layer* q, const void* Xq, const void* xe, int M, void* Y, int ldy,
                            void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The attention half of a decoder layer: what stands between the q/k/v
+ * linears (serq_linear_group) and o_proj's activation quantizer.
+ *
+ *   serq_rope_append   rotates queries and keys by their positions (after an
+ *                      optional RMS norm of each head) and appends keys and
+ *                      values to a paged cache;
+ *   serq_attn_prefill  causal attention of packed prompts, or chunks of them,
+ *                      over the cache;
+ *   serq_attn_decode   one query per sequence over the cache, a prefix that
+ *                      all sequences share being read once for the batch.
+ *
+ * Rows of Q, K, V and O are token rows as the linears write them: bf16, head
+ * h in columns [h D, (h + 1) D), row stride a multiple of 8 elements.  D =
+ * head_dim is 64 or 128.  n_heads is a multiple of the cache's n_kv_heads
+ * with n_heads / n_kv_heads <= 128; query head h reads kv head
+ * h / (n_heads / n_kv_heads).
+ *
+ * The batch (all DEVICE int32, read when the kernels run, so a captured call
+ * follows later changes):
+ *  cu_q        batch + 1 non-decreasing row offsets; sequence b owns rows
+ *              [cu_q[b], cu_q[b+1]).  Rows in front of cu_q[0] or behind
+ *              cu_q[batch] are neither read into a result nor written.
+ *  kv_len      batch: tokens of the sequence in the cache once its rows are
+ *              appended.  Row t of sequence b is at position
+ *              kv_len[b] - (cu_q[b+1] - t); a row whose position is negative
+ *              belongs to no token: serq_rope_append leaves it alone,
+ *              attention writes zeros.
+ *  page_table  batch rows of max_pages page indices, row stride ld_table;
+ *              position p of sequence b lies in page
+ *              page_table[b][p / page_size], slot p % page_size.  Only the
+ *              entries of positions below kv_len[b] are used.
+ * An entry in use that is outside [0, n_pages), or a position past the table's
+ * max_pages, is not followed: such a token is not stored, its key and value
+ * count as zeros in attention (positions past the table are left out), and
+ * serq_device_error reports 5.
+ * Cached keys and values of positions below kv_len[b] have to be finite; what
+ * lies behind them in a page, and other pages, may hold anything.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct serq_rope serq_rope;
+typedef struct serq_kv_cache serq_kv_cache;
+
+typedef enum {
+  SERQ_ROPE_HALF = 0,        /* pairs (i, i + rot_dim / 2)                     */
+  SERQ_ROPE_INTERLEAVED = 1  /* pairs (2 i, 2 i + 1)                           */
+} serq_rope_layout;
+
+typedef enum {
+  SERQ_ROPE_PLAIN = 0,    /* f_i = theta^(-2 i / rot_dim)                      */
+  SERQ_ROPE_LINEAR = 1,   /* f_i / factor (position interpolation)             */
+  SERQ_ROPE_BY_PARTS = 2  /* by the turns r_i = original_len f_i / 2 pi a pair
+                             makes over the original context: with
+                             w = clamp((r_i - low) / (high - low), 0, 1),
+                             f_i' = (1 - w) f_i / factor + w f_i ("NTK by
+                             parts", Peng et al. 2023, YaRN, section 3.2)      */
+} serq_rope_scaling;
+
+typedef struct {
+  int head_dim;         /* 64 or 128                                           */
+  int rot_dim;          /* leading elements of a head that rotate: a multiple of
+                           16, 16 <= rot_dim <= head_dim; default head_dim     */
+  int layout;           /* serq_rope_layout; default SERQ_ROPE_HALF            */
+  int scaling;          /* serq_rope_scaling; default SERQ_ROPE_PLAIN          */
+  double theta;         /* > 1; default 10000                                  */
+  double factor;        /* >= 1; default 1                                     */
+  double original_len;  /* BY_PARTS: original context; default 8192            */
+  double low, high;     /* BY_PARTS: 0 <= low < high; defaults 1, 4            */
+  double amplitude;     /* A, multiplies the rotated elements (YaRN's attention
+                           temperature goes here); > 0; default 1              */
+} serq_rope_opts;
+
+/* Defaults as above with head_dim = rot_dim = 128. */
+void serq_rope_opts_init(serq_rope_opts* opts);
+
+/*
+ * serq_rope_create -- frequencies of a rotation, in fp64 turns per position,
+ * on the current device.  There is no longest position: angles are formed in
+ * fp64 when rows are rotated.  Synchronous; the handle owns its memory.
+ * Errors: SERQ_ERR_INVALID_ARG (null, a value out of its range),
+ * SERQ_ERR_UNSUPPORTED_SHAPE (head_dim, rot_dim), SERQ_ERR_ALLOC,
+ * SERQ_ERR_CUDA, SERQ_ERR_UNSUPPORTED_DEVICE.
+ */
+serq_status serq_rope_create(const serq_rope_opts* opts, serq_rope** out);
+void serq_rope_destroy(serq_rope* rope); /* NULL accepted */
+
+/*
+ * serq_kv_cache_create -- describes a paged cache in memory that the caller
+ * owns and keeps for the handle's life.
+ *  K, V         DEVICE bf16, 16-byte aligned: page p, kv head h, slot s,
+ *               element e at p page_stride + (h page_size + s) head_dim + e.
+ *  n_pages      >= 1
+ *  page_size    16, 32, 64, 128 or 256 tokens
+ *  n_kv_heads   >= 1, n_kv_heads page_size < 2^31
+ *  head_dim     64 or 128
+ *  page_stride  elements, >= n_kv_heads page_size head_dim, a multiple of 8
+ *               (more than that where layers share a page's memory); times 2
+ *               bytes below 2^40
+ * Touches no device memory.  Errors: SERQ_ERR_INVALID_ARG,
+ * SERQ_ERR_UNSUPPORTED_SHAPE (page_size, head_dim), SERQ_ERR_CUDA,
+ * SERQ_ERR_UNSUPPORTED_DEVICE.
+ */
+serq_status serq_kv_cache_create(void* K, void* V, int n_pages, int page_size, int n_kv_heads, int head_dim,
+                                 int64_t page_stride, serq_kv_cache** out);
+void serq_kv_cache_destroy(serq_kv_cache* cache); /* frees the handle, not the pages; NULL accepted */
+
+/*
+ * serq_rope_append -- for every row t of the batch at position p: queries to
+ * Qout, keys and values to the cache, queries and keys rotated by p and, when
+ * q_weight and k_weight are given, RMS-normalised per head first:
+ *   x' = x w / sqrt(mean(x^2) + eps)   (fp32),  then one rounding to bf16.
+ *  Q, K, V      DEVICE bf16, T rows of n_heads, n_kv_heads, n_kv_heads heads.
+ *  q_weight, k_weight  DEVICE bf16[head_dim], both or neither.
+ *  Qout         DEVICE bf16, T rows; Qout = Q with ldqo = ldq rotates in place.
+ * Two rows of one call must not share a cache position, nor two calls that
+ * may run at the same time.  T >= 1, batch >= 1, max_pages >= 1.
+ * One launch, asynchronous on `stream`.
+ */
+serq_status serq_rope_append(const serq_rope* rope, const serq_kv_cache* cache, const void* Q, int ldq,
+                             const void* K, int ldk, const void* V, int ldv, int T, int n_heads,
+                             const void* q_weight, const void* k_weight, float eps, int batch, const int32_t* cu_q,
+                             const int32_t* kv_len, const int32_t* page_table, int max_pages, int ld_table,
+                             void* Qout, int ldqo, void* stream);
+
+/*
+ * serq_attn_prefill -- O[t, h] = sum_j softmax_j(scale q . k_j) v_j over the
+ * cached positions j <= position(t) of the row's sequence; the row's own key
+ * is among them (append first).  fp32 scores, softmax statistics and sums;
+ * the weights of the value product are rounded to bf16.
+ *  scale   finite; usually 1 / sqrt(head_dim).
+ *  max_kv  a bound on kv_len that the work split is chosen by (0: max_pages
+ *          page_size); a longer sequence is still computed whole.
+ *  ws      DEVICE, 16-byte aligned, serq_attn_prefill_ws_bytes(...) bytes for
+ *          the same arguments (NULL where that is 0): scratch that the call
+ *          writes before it reads, and that calls running at the same time
+ *          must not share.
+ *  O       DEVICE bf16, T rows of n_heads heads; must not overlap Q.
+ * Results are the same from call to call (no atomics).  Asynchronous on
+ * `stream`; a wait that gives up is reported by serq_device_error.
+ */
+size_t serq_attn_prefill_ws_bytes(const serq_kv_cache* cache, int T, int n_heads, int batch, int max_pages, int max_kv);
+serq_status serq_attn_prefill(const serq_kv_cache* cache, const void* Q, int ldq, int T, int n_heads, float scale,
+                              int batch, const int32_t* cu_q, const int32_t* kv_len, const int32_t* page_table,
+                              int max_pages, int ld_table, int max_kv, void* ws, size_t ws_bytes, void* O, int ldo,
+                              void* stream);
+
+/*
+ * serq_attn_decode -- the same with one row per sequence: row b attends to all
+ * kv_len[b] cached positions.
+ *  prefix_len  >= 0, a multiple of page_size, <= max_pages page_size: the first
+ *              prefix_len positions of every sequence are the same tokens, in
+ *              the pages of page_table row 0.  They are read once for the whole
+ *              batch; entries of other rows below prefix_len / page_size are
+ *              not used.  kv_len[b] < prefix_len cuts sequence b's part of it.
+ *  max_kv, ws  as above, with serq_attn_decode_ws_bytes.
+ */
+size_t serq_attn_decode_ws_bytes(const serq_kv_cache* cache, int batch, int n_heads, int max_pages, int prefix_len,
+                                 int max_kv);
+serq_status serq_attn_decode(const serq_kv_cache* cache, const void* Q, int ldq, int n_heads, float scale, int batch,
+                             const int32_t* kv_len, const int32_t* page_table, int max_pages, int ld_table,
+                             int prefix_len, int max_kv, void* ws, size_t ws_bytes, void* O, int ldo, void* stream);
 
 #ifdef __cplusplus
 }

@@ -33,14 +33,15 @@ inline cudaError_t smem_limit(const void* kernel, int bytes) {
   return e;
 }
 
-// Status word that kernels set when a bounded wait gives up.  Read and
-// cleared by serq_device_error().
+// Status word that kernels set when a bounded wait gives up or a page table
+// entry in use is invalid.  Read and cleared by serq_device_error().
 enum DeviceStatus : int {
   kDevOk = 0,
   kDevTimeoutProducer = 1,
   kDevTimeoutUnpack = 2,
   kDevTimeoutMma = 3,
   kDevTimeoutEpilogue = 4,
+  kDevBadPage = 5,  // a page index outside the cache, or more keys than the page table's columns hold
 };
 
 // Wall-clock limit of every spin-wait in the kernels (nanoseconds).  Every

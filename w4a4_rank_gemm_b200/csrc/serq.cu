@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -22,6 +23,8 @@
 #include "gptq.cuh"
 #include "quant.cuh"
 #include "mxfp4.cuh"
+#include "rope.cuh"
+#include "attn.cuh"
 
 namespace {
 
@@ -1737,6 +1740,330 @@ serq_status serq_mx_linear(const serq_mx_layer* q, const void* Xq, const void* x
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "serq_mx_linear launch");
   return ok();
+}
+
+}  // extern "C"
+
+// ------------------------------------------- rotation, paged cache, attention
+struct serq_rope {
+  int head_dim, rot, layout, device;
+  float amp;
+  double* turns;  // rot / 2 frequencies, turns per position
+};
+
+struct serq_kv_cache {
+  int n_pages, page_size, page_shift, n_kv_heads, head_dim, device;
+  int64_t page_stride;
+  __nv_bfloat16 *K, *V;
+};
+
+namespace {
+
+serq_status check_handle_device(int device, const char* what) {
+  int dev = -1;
+  cudaGetDevice(&dev);
+  if (dev != device)
+    return fail(SERQ_ERR_INVALID_ARG, "%s was created on device %d, current device is %d", what, device, dev);
+  return SERQ_OK;
+}
+
+// Token rows of `heads` heads: pointer, stride, alignment.
+serq_status check_token_rows(const void* X, int ld, int heads, int D, const char* name) {
+  if (!X) return fail(SERQ_ERR_INVALID_ARG, "null %s", name);
+  if (ld % 8 || ld < heads * D || !aligned16(X))
+    return fail(SERQ_ERR_INVALID_ARG, "%s must be 16-byte aligned with a row stride (%d) of at least %d, a multiple of 8",
+                name, ld, heads * D);
+  return SERQ_OK;
+}
+
+serq_status check_heads(const serq_kv_cache* c, int n_heads) {
+  if (n_heads < 1 || n_heads % c->n_kv_heads)
+    return fail(SERQ_ERR_UNSUPPORTED_SHAPE, "n_heads = %d is not a positive multiple of %d kv heads", n_heads,
+                c->n_kv_heads);
+  if (n_heads / c->n_kv_heads > 128 || n_heads > 65535)
+    return fail(SERQ_ERR_UNSUPPORTED_SHAPE, "n_heads = %d: at most 128 query heads per kv head and 65535 in all", n_heads);
+  return SERQ_OK;
+}
+
+serq_status check_batch(const serq_kv_cache* c, int batch, const int32_t* kv_len, const int32_t* table, int max_pages,
+                        int ld_table) {
+  if (!kv_len || !table) return fail(SERQ_ERR_INVALID_ARG, "null kv_len or page_table");
+  if (batch < 1) return fail(SERQ_ERR_INVALID_ARG, "batch = %d out of range", batch);
+  if (max_pages < 1 || (int64_t)max_pages * c->page_size > 0x7fffffff)
+    return fail(SERQ_ERR_INVALID_ARG, "max_pages = %d out of range", max_pages);
+  if (ld_table < max_pages) return fail(SERQ_ERR_INVALID_ARG, "ld_table (%d) < max_pages (%d)", ld_table, max_pages);
+  return SERQ_OK;
+}
+
+serq::CacheArgs cache_args(const serq_kv_cache* c) {
+  serq::CacheArgs a;
+  a.K = c->K;
+  a.V = c->V;
+  a.page_stride = c->page_stride;
+  a.n_pages = c->n_pages;
+  a.page_shift = c->page_shift;
+  a.n_kv_heads = c->n_kv_heads;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+void serq_rope_opts_init(serq_rope_opts* o) {
+  if (!o) return;
+  o->head_dim = 128;
+  o->rot_dim = 128;
+  o->layout = SERQ_ROPE_HALF;
+  o->scaling = SERQ_ROPE_PLAIN;
+  o->theta = 10000.0;
+  o->factor = 1.0;
+  o->original_len = 8192.0;
+  o->low = 1.0;
+  o->high = 4.0;
+  o->amplitude = 1.0;
+}
+
+serq_status serq_rope_create(const serq_rope_opts* o, serq_rope** out) {
+  if (!out) return fail(SERQ_ERR_INVALID_ARG, "null out");
+  *out = nullptr;
+  if (!o) return fail(SERQ_ERR_INVALID_ARG, "null opts");
+  if (o->head_dim != 64 && o->head_dim != 128)
+    return fail(SERQ_ERR_UNSUPPORTED_SHAPE, "head_dim = %d is not 64 or 128", o->head_dim);
+  if (o->rot_dim < 16 || o->rot_dim % 16 || o->rot_dim > o->head_dim)
+    return fail(SERQ_ERR_UNSUPPORTED_SHAPE, "rot_dim = %d must be a multiple of 16 in [16, head_dim]", o->rot_dim);
+  if (o->layout != SERQ_ROPE_HALF && o->layout != SERQ_ROPE_INTERLEAVED)
+    return fail(SERQ_ERR_INVALID_ARG, "bad layout %d", o->layout);
+  if (o->scaling < SERQ_ROPE_PLAIN || o->scaling > SERQ_ROPE_BY_PARTS)
+    return fail(SERQ_ERR_INVALID_ARG, "bad scaling %d", o->scaling);
+  const bool parts = o->scaling == SERQ_ROPE_BY_PARTS;
+  if (!(o->theta > 1.0 && std::isfinite(o->theta)) || !(o->factor >= 1.0 && std::isfinite(o->factor)) ||
+      !(o->amplitude > 0.0 && std::isfinite(o->amplitude)))
+    return fail(SERQ_ERR_INVALID_ARG, "theta must be > 1, factor >= 1, amplitude > 0, all finite");
+  if (parts && (!(o->original_len > 0.0 && std::isfinite(o->original_len)) || !(o->low >= 0.0) ||
+                !(o->high > o->low && std::isfinite(o->high))))
+    return fail(SERQ_ERR_INVALID_ARG, "scaling by parts needs original_len > 0 and 0 <= low < high");
+  serq_status s;
+  if ((s = check_device())) return s;
+  const int half = o->rot_dim / 2;
+  const double two_pi = 6.283185307179586476925286766559;
+  double turns[64];
+  for (int i = 0; i < half; ++i) {
+    double f = std::pow(o->theta, -2.0 * i / o->rot_dim);
+    if (o->scaling == SERQ_ROPE_LINEAR) f /= o->factor;
+    if (parts) {
+      const double w = std::min(1.0, std::max(0.0, (o->original_len * f / two_pi - o->low) / (o->high - o->low)));
+      f = (1.0 - w) * f / o->factor + w * f;
+    }
+    turns[i] = f / two_pi;
+  }
+  serq_rope* r = new (std::nothrow) serq_rope();
+  if (!r) return fail(SERQ_ERR_ALLOC, "host allocation failed");
+  r->head_dim = o->head_dim;
+  r->rot = o->rot_dim;
+  r->layout = o->layout;
+  r->amp = (float)o->amplitude;
+  cudaGetDevice(&r->device);
+  cudaError_t e = cudaMalloc(&r->turns, half * sizeof(double));
+  if (e != cudaSuccess) {
+    delete r;
+    cudaGetLastError();
+    return fail(SERQ_ERR_ALLOC, "cudaMalloc failed: %s", cudaGetErrorString(e));
+  }
+  e = cudaMemcpy(r->turns, turns, half * sizeof(double), cudaMemcpyHostToDevice);
+  if (e != cudaSuccess) {
+    cudaFree(r->turns);
+    delete r;
+    cudaGetLastError();
+    return cuda_fail(e, "upload of the frequencies");
+  }
+  *out = r;
+  return ok();
+}
+
+void serq_rope_destroy(serq_rope* r) {
+  if (!r) return;
+  cudaFree(r->turns);
+  delete r;
+}
+
+serq_status serq_kv_cache_create(void* K, void* V, int n_pages, int page_size, int n_kv_heads, int head_dim,
+                                 int64_t page_stride, serq_kv_cache** out) {
+  if (!out) return fail(SERQ_ERR_INVALID_ARG, "null out");
+  *out = nullptr;
+  if (!K || !V) return fail(SERQ_ERR_INVALID_ARG, "null K or V");
+  if (head_dim != 64 && head_dim != 128)
+    return fail(SERQ_ERR_UNSUPPORTED_SHAPE, "head_dim = %d is not 64 or 128", head_dim);
+  int shift = 4;
+  while (shift < 8 && (1 << shift) != page_size) ++shift;
+  if ((1 << shift) != page_size)
+    return fail(SERQ_ERR_UNSUPPORTED_SHAPE, "page_size = %d is not 16, 32, 64, 128 or 256", page_size);
+  if (n_pages < 1) return fail(SERQ_ERR_INVALID_ARG, "n_pages = %d out of range", n_pages);
+  if (n_kv_heads < 1 || n_kv_heads > 65535)
+    return fail(SERQ_ERR_INVALID_ARG, "n_kv_heads = %d out of range", n_kv_heads);
+  if (!aligned16(K) || !aligned16(V) || page_stride % 8 || page_stride >= (int64_t(1) << 39) ||
+      page_stride < (int64_t)n_kv_heads * page_size * head_dim)
+    return fail(SERQ_ERR_INVALID_ARG,
+                "K and V must be 16-byte aligned, page_stride (%lld) at least a page and a multiple of 8",
+                (long long)page_stride);
+  serq_status s;
+  if ((s = check_device())) return s;
+  serq_kv_cache* c = new (std::nothrow) serq_kv_cache();
+  if (!c) return fail(SERQ_ERR_ALLOC, "host allocation failed");
+  c->n_pages = n_pages;
+  c->page_size = page_size;
+  c->page_shift = shift;
+  c->n_kv_heads = n_kv_heads;
+  c->head_dim = head_dim;
+  c->page_stride = page_stride;
+  c->K = static_cast<__nv_bfloat16*>(K);
+  c->V = static_cast<__nv_bfloat16*>(V);
+  cudaGetDevice(&c->device);
+  *out = c;
+  return ok();
+}
+
+void serq_kv_cache_destroy(serq_kv_cache* c) { delete c; }
+
+serq_status serq_rope_append(const serq_rope* rope, const serq_kv_cache* cache, const void* Q, int ldq, const void* K,
+                             int ldk, const void* V, int ldv, int T, int n_heads, const void* q_weight,
+                             const void* k_weight, float eps, int batch, const int32_t* cu_q, const int32_t* kv_len,
+                             const int32_t* page_table, int max_pages, int ld_table, void* Qout, int ldqo,
+                             void* stream) {
+  if (!rope || !cache) return fail(SERQ_ERR_INVALID_ARG, "null rotation or cache");
+  serq_status s;
+  const int D = cache->head_dim;
+  if (rope->head_dim != D)
+    return fail(SERQ_ERR_UNSUPPORTED_SHAPE, "the rotation's head_dim (%d) is not the cache's (%d)", rope->head_dim, D);
+  if ((s = check_heads(cache, n_heads))) return s;
+  if (T < 1) return fail(SERQ_ERR_INVALID_ARG, "T = %d out of range", T);
+  if ((s = check_token_rows(Q, ldq, n_heads, D, "Q"))) return s;
+  if ((s = check_token_rows(K, ldk, cache->n_kv_heads, D, "K"))) return s;
+  if ((s = check_token_rows(V, ldv, cache->n_kv_heads, D, "V"))) return s;
+  if ((s = check_token_rows(Qout, ldqo, n_heads, D, "Qout"))) return s;
+  if (!q_weight != !k_weight) return fail(SERQ_ERR_INVALID_ARG, "q_weight and k_weight go together");
+  if (q_weight && (!aligned16(q_weight) || !aligned16(k_weight) || !(eps >= 0.f && std::isfinite(eps))))
+    return fail(SERQ_ERR_INVALID_ARG, "norm weights must be 16-byte aligned and eps finite, not negative");
+  if (!cu_q) return fail(SERQ_ERR_INVALID_ARG, "null cu_q");
+  if ((s = check_batch(cache, batch, kv_len, page_table, max_pages, ld_table))) return s;
+  if ((s = check_device())) return s;
+  if ((s = check_handle_device(rope->device, "the rotation"))) return s;
+  if ((s = check_handle_device(cache->device, "the cache"))) return s;
+  serq::rope::Args a;
+  a.q = static_cast<const __nv_bfloat16*>(Q);
+  a.k = static_cast<const __nv_bfloat16*>(K);
+  a.v = static_cast<const __nv_bfloat16*>(V);
+  a.q_out = static_cast<__nv_bfloat16*>(Qout);
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.ldqo = ldqo;
+  a.qw = static_cast<const __nv_bfloat16*>(q_weight);
+  a.kw = static_cast<const __nv_bfloat16*>(k_weight);
+  a.eps = eps;
+  a.amp = rope->amp;
+  a.turns = rope->turns;
+  a.T = T;
+  a.n_heads = n_heads;
+  a.rot = rope->rot;
+  a.b = {cu_q, kv_len, page_table, batch, max_pages, ld_table};
+  a.c = cache_args(cache);
+  const bool half = rope->layout == SERQ_ROPE_HALF;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = D == 128 ? serq::rope::launch<128>(a, half, sm_count(), st)
+                                 : serq::rope::launch<64>(a, half, sm_count(), st);
+  if (e != cudaSuccess) return cuda_fail(e, "serq_rope_append launch");
+  return ok();
+}
+
+size_t serq_attn_prefill_ws_bytes(const serq_kv_cache* cache, int T, int n_heads, int batch, int max_pages,
+                                  int max_kv) {
+  return 0;
+}
+
+size_t serq_attn_decode_ws_bytes(const serq_kv_cache* cache, int batch, int n_heads, int max_pages, int prefix_len,
+                                 int max_kv) {
+  return 0;
+}
+
+}  // extern "C"
+
+namespace {
+
+serq_status attn_rows(const serq_kv_cache* c, const void* Q, int ldq, int T, int n_heads, float scale, int batch,
+                      const int32_t* cu_q, const int32_t* kv_len, const int32_t* table, int max_pages, int ld_table,
+                      int prefix, void* O, int ldo, void* stream, const char* what) {
+  serq::attn::Args a;
+  a.q = static_cast<const __nv_bfloat16*>(Q);
+  a.o = static_cast<__nv_bfloat16*>(O);
+  a.ldq = ldq;
+  a.ldo = ldo;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.T = T;
+  a.n_heads = n_heads;
+  a.prefix = prefix;
+  a.b = {cu_q, kv_len, table, batch, max_pages, ld_table};
+  a.c = cache_args(c);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = c->head_dim == 128 ? serq::attn::launch_rows<128>(a, st) : serq::attn::launch_rows<64>(a, st);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return ok();
+}
+
+serq_status check_attn(const serq_kv_cache* c, const void* Q, int ldq, int n_heads, float scale, int batch,
+                       const int32_t* kv_len, const int32_t* table, int max_pages, int ld_table, int max_kv,
+                       const void* O, int ldo) {
+  serq_status s;
+  if (!c) return fail(SERQ_ERR_INVALID_ARG, "null cache");
+  if ((s = check_heads(c, n_heads))) return s;
+  if ((s = check_token_rows(Q, ldq, n_heads, c->head_dim, "Q"))) return s;
+  if ((s = check_token_rows(O, ldo, n_heads, c->head_dim, "O"))) return s;
+  if (!std::isfinite(scale)) return fail(SERQ_ERR_INVALID_ARG, "scale must be finite");
+  if ((s = check_batch(c, batch, kv_len, table, max_pages, ld_table))) return s;
+  if (max_kv < 0) return fail(SERQ_ERR_INVALID_ARG, "max_kv = %d out of range", max_kv);
+  return SERQ_OK;
+}
+
+serq_status check_ws(const void* ws, size_t have, size_t need) {
+  if (need && (!ws || !aligned16(ws) || have < need))
+    return fail(SERQ_ERR_INVALID_ARG, "workspace of %zu bytes (16-byte aligned) needed, %zu given", need, ws ? have : 0);
+  return SERQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+serq_status serq_attn_prefill(const serq_kv_cache* cache, const void* Q, int ldq, int T, int n_heads, float scale,
+                              int batch, const int32_t* cu_q, const int32_t* kv_len, const int32_t* page_table,
+                              int max_pages, int ld_table, int max_kv, void* ws, size_t ws_bytes, void* O, int ldo,
+                              void* stream) {
+  serq_status s;
+  if ((s = check_attn(cache, Q, ldq, n_heads, scale, batch, kv_len, page_table, max_pages, ld_table, max_kv, O, ldo)))
+    return s;
+  if (!cu_q) return fail(SERQ_ERR_INVALID_ARG, "null cu_q");
+  if (T < 1) return fail(SERQ_ERR_INVALID_ARG, "T = %d out of range", T);
+  if ((s = check_ws(ws, ws_bytes, serq_attn_prefill_ws_bytes(cache, T, n_heads, batch, max_pages, max_kv)))) return s;
+  if ((s = check_device())) return s;
+  if ((s = check_handle_device(cache->device, "the cache"))) return s;
+  return attn_rows(cache, Q, ldq, T, n_heads, scale, batch, cu_q, kv_len, page_table, max_pages, ld_table, 0, O, ldo,
+                   stream, "serq_attn_prefill launch");
+}
+
+serq_status serq_attn_decode(const serq_kv_cache* cache, const void* Q, int ldq, int n_heads, float scale, int batch,
+                             const int32_t* kv_len, const int32_t* page_table, int max_pages, int ld_table,
+                             int prefix_len, int max_kv, void* ws, size_t ws_bytes, void* O, int ldo, void* stream) {
+  serq_status s;
+  if ((s = check_attn(cache, Q, ldq, n_heads, scale, batch, kv_len, page_table, max_pages, ld_table, max_kv, O, ldo)))
+    return s;
+  if (prefix_len < 0 || prefix_len % cache->page_size || prefix_len / cache->page_size > max_pages)
+    return fail(SERQ_ERR_INVALID_ARG, "prefix_len = %d is not a multiple of the page size within the table", prefix_len);
+  if ((s = check_ws(ws, ws_bytes, serq_attn_decode_ws_bytes(cache, batch, n_heads, max_pages, prefix_len, max_kv))))
+    return s;
+  if ((s = check_device())) return s;
+  if ((s = check_handle_device(cache->device, "the cache"))) return s;
+  return attn_rows(cache, Q, ldq, batch, n_heads, scale, batch, nullptr, kv_len, page_table, max_pages, ld_table, prefix_len,
+                   O, ldo, stream, "serq_attn_decode launch");
 }
 
 }  // extern "C"

@@ -38,6 +38,17 @@ class PrepareOpts(ctypes.Structure):
                 ("out_perm", _vp), ("out_colscale", _vp), ("quantizer", _i)]
 
 
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BY_PARTS = 0, 1, 2
+
+
+class RopeOpts(ctypes.Structure):
+    """serq_rope_opts."""
+    _fields_ = [("head_dim", _i), ("rot_dim", _i), ("layout", _i), ("scaling", _i), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_len", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
 EXPORTS = {
     "serq_prepare_opts_init": (None, [ctypes.POINTER(PrepareOpts)]),
     "serq_prepare_group": (_i, [_i, ctypes.POINTER(_vp), ctypes.POINTER(_i), _i, _vp, _i, ctypes.POINTER(PrepareOpts),
@@ -73,6 +84,19 @@ EXPORTS = {
     "serq_mx_act_scale_bytes": (ctypes.c_size_t, [_i, _i]),
     "serq_mx_quantize_act": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp]),
     "serq_mx_linear": (_i, [_vp, _vp, _vp, _i, _vp, _i, _vp]),
+    "serq_rope_opts_init": (None, [ctypes.POINTER(RopeOpts)]),
+    "serq_rope_create": (_i, [ctypes.POINTER(RopeOpts), ctypes.POINTER(_vp)]),
+    "serq_rope_destroy": (None, [_vp]),
+    "serq_kv_cache_create": (_i, [_vp, _vp, _i, _i, _i, _i, ctypes.c_int64, ctypes.POINTER(_vp)]),
+    "serq_kv_cache_destroy": (None, [_vp]),
+    "serq_rope_append": (_i, [_vp, _vp, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp, ctypes.c_float, _i, _vp, _vp, _vp,
+                              _i, _i, _vp, _i, _vp]),
+    "serq_attn_prefill_ws_bytes": (ctypes.c_size_t, [_vp, _i, _i, _i, _i, _i]),
+    "serq_attn_prefill": (_i, [_vp, _vp, _i, _i, _i, ctypes.c_float, _i, _vp, _vp, _vp, _i, _i, _i, _vp,
+                               ctypes.c_size_t, _vp, _i, _vp]),
+    "serq_attn_decode_ws_bytes": (ctypes.c_size_t, [_vp, _i, _i, _i, _i, _i]),
+    "serq_attn_decode": (_i, [_vp, _vp, _i, _i, ctypes.c_float, _i, _vp, _vp, _i, _i, _i, _i, _vp, ctypes.c_size_t,
+                              _vp, _i, _vp]),
     "serq_silu_mul_quantize": (_i, [_vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp]),
     "serq_flatten_permute": (_i, [_vp, _vp, _i, _i, _i, _vp, _i, _i, _vp]),
     "serq_test_decode_timeout": (_i, [_vp, _vp, _vp, _i, _vp, _i, _i, _vp]),
@@ -570,6 +594,241 @@ def mx_linear(layer: MXLayer, Xq: torch.Tensor, xe: torch.Tensor, Y: Optional[to
     _check(lib.serq_mx_linear(layer.handle, _ptr(Xq), _ptr(xe), M, _ptr(Y), Y.stride(0), _stream(stream)),
            "serq_mx_linear")
     return Y
+
+
+class Rope:
+    """Owner of a position rotation (serq_rope_create): frequencies of
+    rot_dim / 2 pairs, layout "half" or "interleaved", scaling "none",
+    "linear" or "by_parts", on the current device or `device`."""
+
+    _LAYOUT = {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED}
+    _SCALING = {"none": ROPE_PLAIN, "linear": ROPE_LINEAR, "by_parts": ROPE_BY_PARTS}
+
+    def __init__(self, head_dim: int, rot_dim: Optional[int] = None, layout="half", theta: float = 10000.0,
+                 scaling="none", factor: float = 1.0, original_len: float = 8192.0, low: float = 1.0,
+                 high: float = 4.0, amplitude: float = 1.0, device=None):
+        self._h = None
+        o = RopeOpts()
+        lib.serq_rope_opts_init(ctypes.byref(o))
+        o.head_dim, o.rot_dim = head_dim, head_dim if rot_dim is None else rot_dim
+        o.layout = self._LAYOUT[layout.lower()] if isinstance(layout, str) else int(layout)
+        o.scaling = self._SCALING[scaling.lower()] if isinstance(scaling, str) else int(scaling)
+        o.theta, o.factor, o.original_len = theta, factor, original_len
+        o.low, o.high, o.amplitude = low, high, amplitude
+        h = _vp()
+        with torch.cuda.device(device):
+            _check(lib.serq_rope_create(ctypes.byref(o), ctypes.byref(h)), "serq_rope_create")
+        self.head_dim, self.rot_dim = o.head_dim, o.rot_dim
+        self._h = h
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if self._h:
+            lib.serq_rope_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KVCache:
+    """A paged cache of keys and values (serq_kv_cache_create): K and V are
+    bf16 CUDA tensors n_pages x n_kv_heads x page_size x head_dim, allocated
+    here from the sizes or given (dense within a page, the same page stride),
+    and kept alive by this object."""
+
+    def __init__(self, n_pages: Optional[int] = None, page_size: Optional[int] = None,
+                 n_kv_heads: Optional[int] = None, head_dim: Optional[int] = None, device=None,
+                 K: Optional[torch.Tensor] = None, V: Optional[torch.Tensor] = None):
+        self._h = None
+        if (K is None) != (V is None):
+            raise ValueError("K and V go together")
+        if K is None:
+            shape = (n_pages, n_kv_heads, page_size, head_dim)
+            K = torch.empty(shape, dtype=torch.bfloat16, device=device or "cuda")
+            V = torch.empty_like(K)
+        for t, n in ((K, "K"), (V, "V")):
+            if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 4 or not t[0].is_contiguous():
+                raise ValueError(f"{n} must be a 4-D bf16 CUDA tensor, dense within a page")
+        if K.shape != V.shape or K.device != V.device or (K.shape[0] > 1 and K.stride(0) != V.stride(0)):
+            raise ValueError("K and V must have one shape, device and page stride")
+        self.K, self.V = K, V
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = K.shape
+        self.device = K.device
+        stride = K.stride(0) if self.n_pages > 1 else K[0].numel()
+        h = _vp()
+        with torch.cuda.device(self.device):
+            _check(lib.serq_kv_cache_create(_ptr(K), _ptr(V), self.n_pages, self.page_size, self.n_kv_heads,
+                                            self.head_dim, stride, ctypes.byref(h)), "serq_kv_cache_create")
+        self._h = h
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if self._h:
+            lib.serq_kv_cache_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _token_rows(t: torch.Tensor, name: str, cache: KVCache, heads: Optional[int] = None) -> int:
+    """Checks bf16 token rows of whole heads on the cache's device; returns
+    their number of heads."""
+    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.stride(1) != 1 or t.device != cache.device:
+        raise ValueError(f"{name} must be a 2-D bf16 tensor with unit column stride on the cache's device")
+    n = t.shape[1] // cache.head_dim
+    if n * cache.head_dim != t.shape[1] or (heads is not None and n != heads):
+        raise ValueError(f"{name} has {t.shape[1]} columns, not {'whole' if heads is None else heads} heads of "
+                         f"{cache.head_dim}")
+    return n
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+
+
+def _batch_args(cache: KVCache, kv_len: torch.Tensor, page_table: torch.Tensor, cu_q: Optional[torch.Tensor] = None):
+    for t, n, d in ((kv_len, "kv_len", 1), (page_table, "page_table", 2), (cu_q, "cu_q", 1)):
+        if t is not None and (t.dtype != torch.int32 or t.dim() != d or t.stride(-1) != 1 or t.device != cache.device):
+            raise ValueError(f"{n} must be a {d}-D int32 tensor with unit stride on the cache's device")
+    B = kv_len.shape[0]
+    if page_table.shape[0] != B or (cu_q is not None and cu_q.shape[0] != B + 1):
+        raise ValueError("page_table needs a row for each sequence, cu_q one entry more")
+    cols = page_table.shape[1]
+    return B, cols, page_table.stride(0) if B > 1 else cols
+
+
+def _on(cache: KVCache, stream):
+    """Device guard and stream of a call on the cache's device."""
+    return torch.cuda.device(cache.device), stream if stream is not None else torch.cuda.current_stream(cache.device)
+
+
+def _scratch(n: int, cache: KVCache, ws: Optional[torch.Tensor], stream) -> Optional[torch.Tensor]:
+    if ws is None:
+        if n == 0:
+            return None
+        with torch.cuda.stream(stream):
+            return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != cache.device:
+        raise ValueError("ws must be a contiguous uint8 tensor on the cache's device")
+    return ws
+
+
+def _out_like(Q: torch.Tensor, stream) -> torch.Tensor:
+    with torch.cuda.stream(stream):
+        return torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+
+
+def rope_append(rope: Rope, cache: KVCache, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.Tensor,
+                kv_len: torch.Tensor, page_table: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, Qout: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """serq_rope_append: rotated (and normalised, when weights are given)
+    queries are returned, rotated keys and the values go to the cache.  Q, K,
+    V are T x heads * head_dim rows; Qout may be Q."""
+    n_heads = _token_rows(Q, "Q", cache)
+    _token_rows(K, "K", cache, cache.n_kv_heads)
+    _token_rows(V, "V", cache, cache.n_kv_heads)
+    T = Q.shape[0]
+    if K.shape[0] != T or V.shape[0] != T:
+        raise ValueError("Q, K and V must have the same rows")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != torch.bfloat16 or w.shape != (cache.head_dim,) or not w.is_contiguous()
+                              or w.device != cache.device):
+            raise ValueError("norm weights must be contiguous bf16 tensors of head_dim elements")
+    if cu_q is None:
+        raise ValueError("cu_q is needed")
+    B, cols, ldt = _batch_args(cache, kv_len, page_table, cu_q)
+    guard, st = _on(cache, stream)
+    with guard:
+        if Qout is None:
+            Qout = _out_like(Q, st)
+        elif _token_rows(Qout, "Qout", cache, n_heads) and Qout.shape[0] != T:
+            raise ValueError("Qout must have Q's rows")
+        _check(lib.serq_rope_append(rope.handle, cache.handle, _ptr(Q), _row_stride(Q), _ptr(K), _row_stride(K),
+                                    _ptr(V), _row_stride(V), T, n_heads, _ptr(q_weight), _ptr(k_weight), eps, B,
+                                    _ptr(cu_q), _ptr(kv_len), _ptr(page_table), cols, ldt, _ptr(Qout),
+                                    _row_stride(Qout), _vp(st.cuda_stream)), "serq_rope_append")
+    return Qout
+
+
+def attn_prefill_ws(cache: KVCache, T: int, n_heads: int, batch: int, max_pages: int, max_kv: int = 0):
+    """Scratch for attn_prefill calls of these sizes (None where none is
+    needed); calls that may run at the same time need one each."""
+    with torch.cuda.device(cache.device):
+        n = lib.serq_attn_prefill_ws_bytes(cache.handle, T, n_heads, batch, max_pages, max_kv)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
+
+
+def attn_decode_ws(cache: KVCache, batch: int, n_heads: int, max_pages: int, prefix_len: int = 0, max_kv: int = 0):
+    """The same for attn_decode."""
+    with torch.cuda.device(cache.device):
+        n = lib.serq_attn_decode_ws_bytes(cache.handle, batch, n_heads, max_pages, prefix_len, max_kv)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
+
+
+def attn_prefill(cache: KVCache, Q: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
+                 scale: Optional[float] = None, O: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                 max_kv: int = 0, stream=None) -> torch.Tensor:
+    """serq_attn_prefill: causal attention of the packed rows Q (T x heads *
+    head_dim) over their sequences' cached keys; scale defaults to
+    1 / sqrt(head_dim)."""
+    n_heads = _token_rows(Q, "Q", cache)
+    if cu_q is None:
+        raise ValueError("cu_q is needed")
+    B, cols, ldt = _batch_args(cache, kv_len, page_table, cu_q)
+    T = Q.shape[0]
+    guard, st = _on(cache, stream)
+    with guard:
+        if O is None:
+            O = _out_like(Q, st)
+        elif _token_rows(O, "O", cache, n_heads) and O.shape[0] != T:
+            raise ValueError("O must have Q's rows")
+        ws = _scratch(lib.serq_attn_prefill_ws_bytes(cache.handle, T, n_heads, B, cols, max_kv) if ws is None else 0,
+                      cache, ws, st)
+        _check(lib.serq_attn_prefill(cache.handle, _ptr(Q), _row_stride(Q), T, n_heads,
+                                     cache.head_dim ** -0.5 if scale is None else scale, B, _ptr(cu_q), _ptr(kv_len),
+                                     _ptr(page_table), cols, ldt, max_kv, _ptr(ws), 0 if ws is None else ws.numel(),
+                                     _ptr(O), _row_stride(O), _vp(st.cuda_stream)), "serq_attn_prefill")
+    return O
+
+
+def attn_decode(cache: KVCache, Q: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, prefix_len: int = 0,
+                scale: Optional[float] = None, O: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                max_kv: int = 0, stream=None) -> torch.Tensor:
+    """serq_attn_decode: row b of Q attends to sequence b's kv_len[b] cached
+    keys, the first prefix_len of which all sequences share."""
+    n_heads = _token_rows(Q, "Q", cache)
+    B, cols, ldt = _batch_args(cache, kv_len, page_table)
+    if Q.shape[0] != B:
+        raise ValueError("Q needs one row per sequence")
+    guard, st = _on(cache, stream)
+    with guard:
+        if O is None:
+            O = _out_like(Q, st)
+        elif _token_rows(O, "O", cache, n_heads) and O.shape[0] != B:
+            raise ValueError("O must have Q's rows")
+        ws = _scratch(lib.serq_attn_decode_ws_bytes(cache.handle, B, n_heads, cols, prefix_len, max_kv)
+                      if ws is None else 0, cache, ws, st)
+        _check(lib.serq_attn_decode(cache.handle, _ptr(Q), _row_stride(Q), n_heads,
+                                    cache.head_dim ** -0.5 if scale is None else scale, B, _ptr(kv_len),
+                                    _ptr(page_table), cols, ldt, prefix_len, max_kv, _ptr(ws),
+                                    0 if ws is None else ws.numel(), _ptr(O), _row_stride(O),
+                                    _vp(st.cuda_stream)), "serq_attn_decode")
+    return O
 
 
 def device_error() -> int:
