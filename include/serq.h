@@ -732,7 +732,7 @@ serq_status serq_rope_append(const serq_rope* rope, const serq_kv_cache* cache, 
  * cached positions j <= position(t) of the row's sequence; the row's own key
  * is among them (append first).  fp32 scores, softmax statistics and sums;
  * the weights of the value product are rounded to bf16.
- *  scale   finite; usually 1 / sqrt(head_dim).
+ *  scale   |scale| <= 1e6; usually 1 / sqrt(head_dim).
  *  max_kv  a bound on kv_len that the work split is chosen by (0: max_pages
  *          page_size); a longer sequence is still computed whole.
  *  ws      DEVICE, 16-byte aligned, serq_attn_prefill_ws_bytes(...) bytes for

@@ -1,0 +1,642 @@
+// Attention of many rows on the tensor cores: prompts (causal), and the
+// shared prefix of a decode batch.
+//
+//   S = Q K^T,  P = 2^(c S - m),  O += P V,  l += sum P,  c = scale log2 e
+//
+// One pass over the keys per 128-row tile with the running maximum m and sum
+// l of each row; O and S never leave tensor memory and registers.
+//
+// Rows of a tile are (token, query head of the kv head's group): all heads of
+// a group read the same keys, so 128 / g tokens x g heads share one tile, and
+// one token of a whole group fills g rows.  A CTA works on a pair of tiles (A:
+// the earlier tokens, B: the next) that share the K and V tiles it streams:
+// while the tensor core computes one tile's products the other's softmax runs.
+//
+// TMEM (512 columns): S_A, S_B (128 fp32 columns each; P_X in bf16 takes the
+// first 64 columns of S_X once S_X is in registers), O_A, O_B (D each).
+//
+// Warps: 0-3 softmax of A (one row per thread), 4-7 of B, 8 loads, 9 MMAs
+// (10 and 11 only fill their warpgroup).
+// Persistent: a CTA takes work items (tile pair, kv head, key split) and the
+// next item's Q, K and first scores overlap the epilogue of the last one.
+#pragma once
+
+#include <algorithm>
+
+#include "attn.cuh"
+
+namespace serq {
+namespace attn {
+
+constexpr int kTileRows = 128;  // rows of a tile
+constexpr int kTileKeys = 128;  // keys of a step
+// Three warpgroups.  Launched with 168 registers a thread (384 x 168 = 64512);
+// loads and MMAs keep 88, the softmax threads take 208, each holding a row of
+// 128 scores: 128 x 88 + 256 x 208 = 64512.
+constexpr int kTcThreads = 384;
+constexpr int kRegsIssue = 88, kRegsSoftmax = 208;
+static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= kTcThreads * 168, "register split");
+constexpr float kLazyMax = 8.0f;  // log2: how far a row's scores may exceed the maximum in use
+
+struct TcArgs {
+  __nv_bfloat16* o;  // po == nullptr
+  long long ldo;
+  float* po;         // partial outputs [split][token][head][D], normalised
+  float* plse;       // and log2 of their sums [split][token][head], -inf: nothing
+  float c;           // |scale| log2 e, never 0
+  int neg;           // scale < 0: the product is taken with -Q
+  int T, n_heads, group, tokens;  // tokens: per tile, 128 / group
+  int splits;
+  int prefix;        // > 0: decode rows; every row is at sequence 0's first `prefix` keys, up to its own kv_len
+  BatchArgs b;
+  CacheArgs c_;
+};
+
+struct Item {
+  int done;
+  int j0, endA, endB;  // steps [j0, end) of 128 keys; end <= j0: none
+  int row0, n_tok;     // first token row, tokens of the pair
+  int lim0;            // keys that the first token sees (causal: one more for each next)
+  int kv_end;          // keys that exist
+  int kvh, split, seq;
+};
+
+template <int D>
+struct TcLayout {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTile = 128 * D * 2;  // bytes of a Q tile, and of a K or V step
+  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr int oQ = 0;
+  static constexpr int oKV = 2 * kTile;
+  static constexpr int oItem = oKV + kSlots * kTile;
+  static constexpr int oBar = oItem + 2 * 64;
+  static constexpr int kBars = 2 * kSlots + 2 * 4 + 4 + 1;
+  static constexpr int oMisc = oBar + kBars * 8;
+  static constexpr int kAlloc = oMisc + 16 + 1024;
+};
+static_assert(sizeof(Item) <= 64, "item slot");
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Decodes work item w (the whole warp calls): items run over (tile pair, last
+// first), kv head, key split.
+__device__ __forceinline__ void decode_item(const TcArgs& a, int w, int lane, Item& it) {
+  const int pair = 2 * a.tokens;
+  it.split = w % a.splits;
+  w /= a.splits;
+  it.kvh = w % a.c_.n_kv_heads;
+  w /= a.c_.n_kv_heads;
+  const int cap = a.b.max_pages << a.c_.page_shift;
+  it.done = 0;
+  int seq = 0, tile = w, first = 0, n = 0;
+  if (a.prefix) {
+    n = a.T;
+    const int tiles = ceil_div(n, pair);
+    if (w >= tiles) it.done = 1;
+  } else {
+    // the w-th tile pair from the back
+    int total = 0;
+    for (int b0 = 0; b0 < a.b.batch; b0 += 32) {
+      const int b = b0 + lane;
+      const int nb = b < a.b.batch ? max(0, a.b.cu_q[b + 1] - a.b.cu_q[b]) : 0;
+      total += __reduce_add_sync(0xffffffffu, ceil_div(nb, pair));
+    }
+    if (w >= total) {
+      it.done = 1;
+    } else {
+      int left = total - 1 - w;
+      for (int b0 = 0; b0 < a.b.batch; b0 += 32) {
+        const int b = b0 + lane;
+        const int nb = b < a.b.batch ? max(0, a.b.cu_q[b + 1] - a.b.cu_q[b]) : 0;
+        const int mine = ceil_div(nb, pair);
+        int incl = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += v;
+        }
+        const int sum = __shfl_sync(0xffffffffu, incl, 31);
+        if (left < sum) {
+          const uint32_t hit = __ballot_sync(0xffffffffu, left < incl);
+          const int src = __ffs(hit) - 1;
+          seq = b0 + src;
+          tile = left - (__shfl_sync(0xffffffffu, incl, src) - __shfl_sync(0xffffffffu, mine, src));
+          n = __shfl_sync(0xffffffffu, nb, src);
+          break;
+        }
+        left -= sum;
+      }
+      first = a.b.cu_q[seq];
+    }
+  }
+  if (it.done) return;
+  it.row0 = first + tile * pair;
+  it.n_tok = min(pair, n - tile * pair);
+  int limA, limB;  // most keys that a row of the tile sees
+  if (a.prefix) {
+    int m = 0;
+    for (int b = lane; b < a.b.batch; b += 32) m = max(m, min(a.b.kv_len[b], a.prefix));
+    it.kv_end = __reduce_max_sync(0xffffffffu, m);
+    it.lim0 = 0;
+    limA = limB = it.kv_end;
+  } else {
+    const int kv = a.b.kv_len[seq];
+    it.kv_end = max(0, min(kv, cap));
+    if (kv > cap && lane == 0) note_bad_page();
+    it.lim0 = kv - n + tile * pair + 1;
+    limA = min(it.kv_end, it.lim0 + min(a.tokens, it.n_tok) - 1);
+    limB = min(it.kv_end, it.lim0 + it.n_tok - 1);
+  }
+  const int nA = ceil_div(max(limA, 0), kTileKeys);
+  const int nB = it.n_tok > a.tokens ? ceil_div(max(limB, 0), kTileKeys) : 0;
+  const int steps = max(nA, nB);
+  const int per = ceil_div(steps, a.splits);
+  it.j0 = it.split * per;
+  it.endA = min(nA, it.j0 + per);
+  it.endB = min(nB, it.j0 + per);
+  it.seq = seq;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    k_attn(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+           const __grid_constant__ CUtensorMap tmV, const TcArgs a) {
+  using L = TcLayout<D>;
+  constexpr uint32_t kS = 0, kO = 256;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Item* items = reinterpret_cast<Item*>(smem + L::oItem);  // two, 64 bytes apart
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::oBar);
+  uint64_t* kv_full = bar;
+  uint64_t* kv_empty = kv_full + L::kSlots;
+  uint64_t* q_full = kv_empty + L::kSlots;  // [2] tile X's rows landed
+  uint64_t* q_empty = q_full + 2;           // [2] the item's last scores of X are computed
+  uint64_t* s_full = q_empty + 2;           // [2] scores ready (and every MMA before them)
+  uint64_t* p_full = s_full + 2;            // [2] weights written (and O rescaled)
+  uint64_t* o_full = p_full + 2;            // [2] the item's last product of X is done
+  uint64_t* it_full = o_full + 2;           // [2]
+  uint64_t* it_empty = it_full + 2;         // [2]
+  uint64_t* drain = it_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::oMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::oMisc + 4);
+  auto item_at = [&](int i) -> Item& {
+    return *reinterpret_cast<Item*>(reinterpret_cast<uint8_t*>(items) + (i & 1) * 64);
+  };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kSlots; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&q_full[x], 1);
+      mbar_init(&q_empty[x], 1);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);
+      mbar_init(&o_full[x], 1);
+      mbar_init(&it_full[x], 1);
+      mbar_init(&it_empty[x], 9);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc<1>(tmem_slot, 512);
+    tmem_relinquish<1>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+  if (warp == 8) {
+    // --------------------------------------------------------------- loads
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    grid_dep_wait();
+    const int page = 1 << a.c_.page_shift;
+    const int box = min(page, kTileKeys);         // rows per copy
+    const int copies = kTileKeys / box * L::kHalves;  // per step and operand
+    uint32_t slot = 0, slot_ph = 0, qn[2] = {0, 0};
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      Item it;
+      // every other round backwards: the items come in falling cost, so that
+      // each CTA's sum stays near the mean
+      decode_item(a, i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, it);
+      ok = __all_sync(0xffffffffu, mbar_wait(&it_empty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, kDevTimeoutProducer));
+      if (!ok) break;
+      if (lane == 0) {
+        item_at(i) = it;
+        mbar_arrive(&it_full[i & 1]);
+      }
+      if (it.done) break;
+      const int32_t* table = a.b.table + (long long)it.seq * a.b.ldt;
+      const int end = max(it.endA, it.endB);
+#pragma unroll 1
+      for (int x = 0; x < 2 && ok; ++x) {
+        if ((x ? it.endB : it.endA) <= it.j0) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[x], (qn[x] & 1) ^ 1, abort_flag, kDevTimeoutProducer));
+        if (!ok) break;
+        ++qn[x];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full[x], a.tokens * a.group * D * 2);
+          for (int h = 0; h < L::kHalves; ++h)
+            tma_load_3d(smem + L::oQ + x * L::kTile + h * (L::kTile / L::kHalves), &tmQ, &q_full[x], 64 * h,
+                        it.kvh * a.group, it.row0 + x * a.tokens);
+        }
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int j = it.j0; j < end && ok; ++j) {
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[slot], slot_ph ^ 1, abort_flag, kDevTimeoutProducer));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], L::kTile);
+          __syncwarp();
+          if (lane < copies) {
+            const int half = lane & (L::kHalves - 1), r = lane / L::kHalves * box;
+            const int key = j * kTileKeys + r;
+            // past the keys that exist: the copy fills zeros from outside the map
+            int pg = a.c_.n_pages;
+            if (key < it.kv_end) {
+              const int e = table[key >> a.c_.page_shift];
+              if (e >= 0 && e < a.c_.n_pages) pg = e;
+              else note_bad_page();
+            }
+            tma_load_3d(smem + L::oKV + slot * L::kTile + half * (L::kTile / L::kHalves) + r * 128, v ? &tmV : &tmK,
+                        &kv_full[slot], 64 * half, (it.kvh << a.c_.page_shift) + (key & (page - 1)), pg);
+          }
+          __syncwarp();
+          if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
+        }
+      }
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------- MMAs
+    const uint32_t idesc_qk = umma_idesc_bf16(128, kTileKeys, false, a.neg);
+    constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D, true, false);
+    constexpr int kHalfBytes = L::kTile / L::kHalves;
+    uint32_t slot = 0, slot_ph = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
+    bool ok = true;
+    auto wait = [&](uint64_t* b, uint32_t ph) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(b, ph, abort_flag, kDevTimeoutMma));
+      return ok;
+    };
+    auto scores = [&](int x, uint32_t ks) {
+      const uint64_t dq = umma_desc_k_sw128(smem_u32(smem + L::oQ + x * L::kTile));
+      const uint64_t dk = umma_desc_k_sw128(smem_u32(smem + L::oKV + ks * L::kTile));
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
+        umma_bf16_ss(tmem + kS + 128u * x, dq + off, dk + off, idesc_qk, k > 0);
+      }
+    };
+    auto values = [&](int x, uint32_t vs, bool acc) {
+      const uint64_t dv = umma_desc_mn_sw128(smem_u32(smem + L::oKV + vs * L::kTile), kHalfBytes);
+#pragma unroll
+      for (int k = 0; k < kTileKeys / 16; ++k)
+        umma_bf16_ts(tmem + kO + (uint32_t)(D * x), tmem + kS + 128u * x + 8u * k, dv + (uint64_t)(128 * k), idesc_pv,
+                     acc || k > 0);
+    };
+    for (int i = 0; ok; ++i) {
+      if (!wait(&it_full[i & 1], (i >> 1) & 1)) break;
+      const Item it = item_at(i);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&it_empty[i & 1]);
+      if (it.done) break;
+      const int end = max(it.endA, it.endB);
+      if (end <= it.j0) continue;
+      auto last = [&](int x) { return x ? it.endB : it.endA; };
+      // scores of the first step
+      if (!wait(&kv_full[slot], slot_ph)) break;
+      for (int x = 0; x < 2; ++x) {
+        if (it.j0 >= last(x)) continue;
+        if (!wait(&q_full[x], qn[x]++ & 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          scores(x, slot);
+          umma_commit<1>(&s_full[x]);
+          if (it.j0 + 1 == last(x)) umma_commit<1>(&q_empty[x]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (elect_one()) umma_commit<1>(&kv_empty[slot]);
+      __syncwarp();
+      if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
+      for (int j = it.j0; j < end; ++j) {
+        const uint32_t vs = slot;
+        if (!wait(&kv_full[slot], slot_ph)) break;
+        if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
+        const uint32_t ks = slot;
+        if (j + 1 < end) {
+          if (!wait(&kv_full[slot], slot_ph)) break;
+          if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
+        }
+        // rows of V behind the last key, up to the end of its page, may hold
+        // anything, and 0 times a NaN is one: zero them
+        const int have = it.kv_end - j * kTileKeys;
+        if (have < kTileKeys) {
+          const int upto = min(kTileKeys, (have + (1 << a.c_.page_shift) - 1) >> a.c_.page_shift << a.c_.page_shift);
+          const int n = (upto - have) * (D / 8);  // 16-byte chunks
+          for (int e = lane; e < n; e += 32) {
+            const int r = have + e / (D / 8), cch = e % (D / 8);
+            *reinterpret_cast<uint4*>(smem + L::oKV + vs * L::kTile + (cch >> 3) * kHalfBytes + r * 128 + (cch & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        for (int x = 0; x < 2; ++x) {
+          if (j >= last(x)) continue;
+          if (!wait(&p_full[x], pn[x]++ & 1)) break;
+          tc_fence_after();
+          if (elect_one()) {
+            values(x, vs, j > it.j0);
+            if (j + 1 < last(x)) {
+              scores(x, ks);
+              umma_commit<1>(&s_full[x]);
+              if (j + 2 == last(x)) umma_commit<1>(&q_empty[x]);
+            } else {
+              umma_commit<1>(&o_full[x]);
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) {
+          umma_commit<1>(&kv_empty[vs]);
+          if (j + 1 < end) umma_commit<1>(&kv_empty[ks]);
+        }
+        __syncwarp();
+      }
+    }
+    // every MMA issued has completed before TMEM and shared memory are freed
+    if (elect_one()) {
+      umma_commit<1>(drain);
+      mbar_wait(drain, 0, nullptr, kDevTimeoutMma);
+    }
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ------------------------------------------------------------- softmax
+    const int x = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tS = tmem + lanes + kS + 128u * x, tO = tmem + lanes + kO + (uint32_t)(D * x);
+    const int tok = row / a.group, head = row - tok * a.group;
+    uint32_t sn = 0, on = 0;
+    for (int i = 0;; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&it_full[i & 1], (i >> 1) & 1, abort_flag, kDevTimeoutEpilogue))) break;
+      const Item it = item_at(i);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&it_empty[i & 1]);
+      if (it.done) break;
+      const int end = x ? it.endB : it.endA;
+      const int ti = x * a.tokens + tok;  // token within the pair
+      const int t = it.row0 + ti;
+      const bool valid = tok < a.tokens && ti < it.n_tok && t >= 0 && t < a.T;
+      // keys this row sees; a row that is no row masks nothing
+      int lim = 0x7fffffff;
+      if (valid) lim = a.prefix ? min(a.b.kv_len[t], it.kv_end) : min(it.lim0 + ti, it.kv_end);
+      const int warp_lim = __reduce_min_sync(0xffffffffu, lim);
+      float mc = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = it.j0; j < end; ++j) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], sn++ & 1, abort_flag, kDevTimeoutEpilogue));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t r[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(tS + 32u * q, r[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld_wait_regs(r[q]);
+        const int base = j * kTileKeys;
+        if (base + kTileKeys > warp_lim) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (base + 32 * q + e >= lim) r[q][e] = 0xff800000u;  // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mx[q] = __uint_as_float(r[q][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) mx[q] = fmaxf(mx[q], __uint_as_float(r[q][e]));
+        }
+        const float cand = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
+        // the maximum in use follows only when it falls behind by 2^8: weights
+        // up to 2^8 cost nothing in bf16 or fp32, and most steps leave O alone
+        const bool grow = valid && cand > mc + kLazyMax;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? ex2(mc - cand) : 1.0f;
+          if (grow) {
+            mc = cand;
+            l *= f;
+          }
+          if (j > it.j0) {
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(tO + 16u * q, o);
+              tmem_ld_wait_regs(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x16(tO + 16u * q, o);
+            }
+          }
+        }
+        const float sub = mc == -INFINITY ? 0.f : -mc;
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 s2 = make_float2(__uint_as_float(r[q][2 * e]), __uint_as_float(r[q][2 * e + 1]));
+            const float2 y = fma2(s2, make_float2(a.c, a.c), make_float2(sub, sub));
+            const float2 p = make_float2(ex2(y.x), ex2(y.y));
+            if (e & 1) sum1 = add2(sum1, p);
+            else sum0 = add2(sum0, p);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
+            w[e] = reinterpret_cast<const uint32_t&>(h);
+          }
+          tmem_st_32x32b_x16(tS + 16u * q, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+      }
+      if (!ok) break;
+      // -------------------------------------------------------- epilogue
+      const bool any = end > it.j0;
+      if (any) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[x], on++ & 1, abort_flag, kDevTimeoutEpilogue));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const float inv = l > 0.f ? 1.0f / l : 0.f;
+      const int h = it.kvh * a.group + head;
+      if (a.po != nullptr) {
+        const long long at = ((long long)it.split * a.T + t) * a.n_heads + h;
+        if (valid) a.plse[at] = l > 0.f ? mc + log2f(l) : -INFINITY;
+        if (any) {
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(tO + 32u * q, o);
+            tmem_ld_wait_regs(o);
+            if (valid && l > 0.f) {
+              float4* dst = reinterpret_cast<float4*>(a.po + at * D + 32 * q);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                     __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+            }
+          }
+        }
+      } else {
+        __nv_bfloat16* dst = a.o + (long long)t * a.ldo + (long long)h * D;
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          if (any) {
+            tmem_ld_32x32b_x32(tO + 32u * q, o);
+            tmem_ld_wait_regs(o);
+          }
+          if (valid) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              // a row that saw no key has inv = 0 and is written as zeros
+              const float v0 = l > 0.f ? __uint_as_float(o[2 * e]) * inv : 0.f;
+              const float v1 = l > 0.f ? __uint_as_float(o[2 * e + 1]) * inv : 0.f;
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(v0, v1);
+              w[e] = reinterpret_cast<const uint32_t&>(b2);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              reinterpret_cast<uint4*>(dst + 32 * q)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          }
+        }
+      }
+      // the next item's first product overwrites O: its weights are only
+      // signalled after these loads
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) {
+    // let copies already issued land before the shared memory is released
+    const unsigned long long t0 = global_ns();
+    while (global_ns() - t0 < 100000ull) {
+    }
+  }
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc<1>(tmem, 512);
+  }
+}
+
+// Joins partial outputs: O = sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M).
+// One warp per (row, head); splits whose part is empty are not read.
+template <int D>
+__global__ void __launch_bounds__(128) k_merge(const float* po, const float* plse, int splits, int T, int n_heads,
+                                               const int32_t* cu_q, int batch, __nv_bfloat16* o, long long ldo) {
+  const int lane = threadIdx.x & 31;
+  const long long rows = (long long)T * n_heads;
+  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  grid_dep_wait();
+  if (r >= rows) return;
+  const int t = (int)(r / n_heads), h = (int)(r % n_heads);
+  if (cu_q != nullptr && (t < cu_q[0] || t >= cu_q[batch])) return;
+  float m = -INFINITY;
+  for (int s = lane; s < splits; s += 32) m = fmaxf(m, plse[s * rows + r]);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  constexpr int E = D / 32;
+  float acc[E] = {}, z = 0.f;
+  if (m != -INFINITY) {
+    for (int s = 0; s < splits; ++s) {
+      const float ls = plse[s * rows + r];
+      if (ls == -INFINITY) continue;
+      const float w = ex2(ls - m);
+      z += w;
+      const float* src = po + (s * rows + r) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += w * src[e];
+    }
+  }
+  const float inv = z > 0.f ? 1.f / z : 0.f;
+  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(o + t * ldo + (long long)h * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) dst[e] = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+}
+
+// Work split of a call with at most `pairs` tile pairs per kv head: enough key
+// splits to fill the SMs, none shorter than 512 keys.
+inline int tc_splits(long long pairs, int n_kv_heads, long long max_kv, int sms) {
+  const long long items = pairs * n_kv_heads;
+  const long long steps = (max_kv + kTileKeys - 1) / kTileKeys;
+  return (int)std::max(1ll, std::min({sms / std::max(1ll, items), steps / 4, 64ll}));
+}
+
+template <int D>
+inline cudaError_t launch_tc(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const TcArgs& a,
+                             long long items, int sms, cudaStream_t st) {
+  auto kern = k_attn<D>;
+  const cudaError_t e = smem_limit(reinterpret_cast<const void*>(kern), TcLayout<D>::kAlloc);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(items, sms));
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = TcLayout<D>::kAlloc;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tmQ, tmK, tmV, a);
+}
+
+template <int D>
+inline cudaError_t launch_merge(const float* po, const float* plse, int splits, int T, int n_heads, const int32_t* cu_q,
+                                int batch, __nv_bfloat16* o, long long ldo, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((long long)T * n_heads + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_merge<D>, po, plse, splits, T, n_heads, cu_q, batch, o, ldo);
+}
+
+}  // namespace attn
+}  // namespace serq

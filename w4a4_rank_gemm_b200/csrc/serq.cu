@@ -25,6 +25,7 @@
 #include "mxfp4.cuh"
 #include "rope.cuh"
 #include "attn.cuh"
+#include "attn_tc.cuh"
 
 namespace {
 
@@ -95,6 +96,21 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, u
   CUresult r = fn(m, dtype, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+// 3-D tensor [slices][rows][inner] of bf16, strides in bytes, in the 128-byte
+// swizzle (box inner 64 elements).
+bool make_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t slices,
+                      uint64_t row_stride, uint64_t slice_stride, uint32_t box_rows, uint32_t box_slices) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {inner, rows, slices};
+  cuuint64_t strides[2] = {row_stride, slice_stride};
+  cuuint32_t box[3] = {64, box_rows, box_slices};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -1755,6 +1771,7 @@ struct serq_kv_cache {
   int n_pages, page_size, page_shift, n_kv_heads, head_dim, device;
   int64_t page_stride;
   __nv_bfloat16 *K, *V;
+  CUtensorMap tmK, tmV;  // box: 64 elements x min(page_size, 128) slots of one head
 };
 
 namespace {
@@ -1919,6 +1936,13 @@ serq_status serq_kv_cache_create(void* K, void* V, int n_pages, int page_size, i
   c->K = static_cast<__nv_bfloat16*>(K);
   c->V = static_cast<__nv_bfloat16*>(V);
   cudaGetDevice(&c->device);
+  const uint32_t box = page_size < 128 ? page_size : 128;
+  for (int i = 0; i < 2; ++i)
+    if (!make_map_bf16_3d(i ? &c->tmV : &c->tmK, i ? V : K, head_dim, (uint64_t)n_kv_heads * page_size, n_pages,
+                          (uint64_t)head_dim * 2, (uint64_t)page_stride * 2, box, 1)) {
+      delete c;
+      return fail(SERQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
+    }
   *out = c;
   return ok();
 }
@@ -1976,11 +2000,6 @@ serq_status serq_rope_append(const serq_rope* rope, const serq_kv_cache* cache, 
   return ok();
 }
 
-size_t serq_attn_prefill_ws_bytes(const serq_kv_cache* cache, int T, int n_heads, int batch, int max_pages,
-                                  int max_kv) {
-  return 0;
-}
-
 size_t serq_attn_decode_ws_bytes(const serq_kv_cache* cache, int batch, int n_heads, int max_pages, int prefix_len,
                                  int max_kv) {
   return 0;
@@ -1989,6 +2008,10 @@ size_t serq_attn_decode_ws_bytes(const serq_kv_cache* cache, int batch, int n_he
 }  // extern "C"
 
 namespace {
+
+// |scale| log2 e; a zero scale becomes the smallest normal number, so that a
+// masked score stays -inf instead of turning into a NaN.
+float attn_scale(float scale) { return std::max(std::fabs(scale) * 1.4426950408889634f, 1.17549435e-38f); }
 
 serq_status attn_rows(const serq_kv_cache* c, const void* Q, int ldq, int T, int n_heads, float scale, int batch,
                       const int32_t* cu_q, const int32_t* kv_len, const int32_t* table, int max_pages, int ld_table,
@@ -2018,7 +2041,7 @@ serq_status check_attn(const serq_kv_cache* c, const void* Q, int ldq, int n_hea
   if ((s = check_heads(c, n_heads))) return s;
   if ((s = check_token_rows(Q, ldq, n_heads, c->head_dim, "Q"))) return s;
   if ((s = check_token_rows(O, ldo, n_heads, c->head_dim, "O"))) return s;
-  if (!std::isfinite(scale)) return fail(SERQ_ERR_INVALID_ARG, "scale must be finite");
+  if (!(std::fabs(scale) <= 1e6f)) return fail(SERQ_ERR_INVALID_ARG, "scale must be within +-1e6");
   if ((s = check_batch(c, batch, kv_len, table, max_pages, ld_table))) return s;
   if (max_kv < 0) return fail(SERQ_ERR_INVALID_ARG, "max_kv = %d out of range", max_kv);
   return SERQ_OK;
@@ -2032,7 +2055,38 @@ serq_status check_ws(const void* ws, size_t have, size_t need) {
 
 }  // namespace
 
+namespace {
+
+// Tile pairs per kv head that a prompt call can have at most, and its key splits.
+struct PrefillPlan {
+  int group, tokens, splits;
+  long long pairs;
+  size_t ws;
+};
+PrefillPlan prefill_plan(const serq_kv_cache* c, int T, int n_heads, int batch, int max_pages, int max_kv) {
+  PrefillPlan p;
+  p.group = n_heads / c->n_kv_heads;
+  p.tokens = serq::attn::kTileRows / p.group;
+  p.pairs = T / (2 * p.tokens) + std::min(batch, T);
+  const long long cap = (long long)max_pages * c->page_size;
+  p.splits = serq::attn::tc_splits(p.pairs, c->n_kv_heads, max_kv ? std::min<long long>(max_kv, cap) : cap, sm_count());
+  p.ws = p.splits > 1 ? (size_t)p.splits * T * n_heads * (c->head_dim + 1) * sizeof(float) : 0;
+  return p;
+}
+
+bool map_rows(CUtensorMap* m, const void* Q, int ldq, int T, int n_heads, int D, int group, int tokens) {
+  return make_map_bf16_3d(m, Q, D, n_heads, T, (uint64_t)D * 2, (uint64_t)ldq * 2, group, tokens);
+}
+
+}  // namespace
+
 extern "C" {
+
+size_t serq_attn_prefill_ws_bytes(const serq_kv_cache* cache, int T, int n_heads, int batch, int max_pages,
+                                  int max_kv) {
+  if (!cache || T < 1 || batch < 1 || max_pages < 1 || max_kv < 0 || check_heads(cache, n_heads)) return 0;
+  return prefill_plan(cache, T, n_heads, batch, max_pages, max_kv).ws;
+}
 
 serq_status serq_attn_prefill(const serq_kv_cache* cache, const void* Q, int ldq, int T, int n_heads, float scale,
                               int batch, const int32_t* cu_q, const int32_t* kv_len, const int32_t* page_table,
@@ -2046,8 +2100,35 @@ serq_status serq_attn_prefill(const serq_kv_cache* cache, const void* Q, int ldq
   if ((s = check_ws(ws, ws_bytes, serq_attn_prefill_ws_bytes(cache, T, n_heads, batch, max_pages, max_kv)))) return s;
   if ((s = check_device())) return s;
   if ((s = check_handle_device(cache->device, "the cache"))) return s;
-  return attn_rows(cache, Q, ldq, T, n_heads, scale, batch, cu_q, kv_len, page_table, max_pages, ld_table, 0, O, ldo,
-                   stream, "serq_attn_prefill launch");
+  const int D = cache->head_dim;
+  const PrefillPlan p = prefill_plan(cache, T, n_heads, batch, max_pages, max_kv);
+  CUtensorMap tmQ;
+  if (!map_rows(&tmQ, Q, ldq, T, n_heads, D, p.group, p.tokens))
+    return fail(SERQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for Q");
+  serq::attn::TcArgs a;
+  a.o = static_cast<__nv_bfloat16*>(O);
+  a.ldo = ldo;
+  a.po = p.ws ? static_cast<float*>(ws) : nullptr;
+  a.plse = p.ws ? a.po + (size_t)p.splits * T * n_heads * D : nullptr;
+  a.c = attn_scale(scale);
+  a.neg = scale < 0.f;
+  a.T = T;
+  a.n_heads = n_heads;
+  a.group = p.group;
+  a.tokens = p.tokens;
+  a.splits = p.splits;
+  a.prefix = 0;
+  a.b = {cu_q, kv_len, page_table, batch, max_pages, ld_table};
+  a.c_ = cache_args(cache);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const long long items = p.pairs * cache->n_kv_heads * p.splits;
+  cudaError_t e = D == 128 ? serq::attn::launch_tc<128>(tmQ, cache->tmK, cache->tmV, a, items, sm_count(), st)
+                           : serq::attn::launch_tc<64>(tmQ, cache->tmK, cache->tmV, a, items, sm_count(), st);
+  if (e == cudaSuccess && p.ws)
+    e = D == 128 ? serq::attn::launch_merge<128>(a.po, a.plse, p.splits, T, n_heads, cu_q, batch, a.o, ldo, st)
+                 : serq::attn::launch_merge<64>(a.po, a.plse, p.splits, T, n_heads, cu_q, batch, a.o, ldo, st);
+  if (e != cudaSuccess) return cuda_fail(e, "serq_attn_prefill launch");
+  return ok();
 }
 
 serq_status serq_attn_decode(const serq_kv_cache* cache, const void* Q, int ldq, int n_heads, float scale, int batch,
