@@ -1,0 +1,526 @@
+// Decode attention: one query token per sequence over the paged cache, bound
+// by the bytes of K and V.
+//
+// Work is counted in blocks of 64 keys of one (sequence, kv head, 16 query
+// heads), laid end to end over the batch; CTA c of G takes the c-th equal
+// share, whatever the lengths are, as the streaming GEMV shares the weights.
+// A share is a run of segments: the end of one pair's keys, whole pairs, the
+// beginning of another's.  Whole pairs are finished here; the first and last
+// segment of a share may be partial and go to the workspace (slots 2c and
+// 2c + 1), to be joined in share order by k_join.
+//
+// Warp 8 streams K and V blocks by TMA into a ring (192 KB in flight per SM),
+// across segment boundaries.  Warps 0-3 take the even blocks, 4-7 the odd
+// ones, 16 keys each: scores and output by mma.sync m16n8k16 with the group's
+// query heads as the 16 rows.  Their use of the tensor core is far below its
+// rate (16 flop per byte read), so nothing is gained by tcgen05 here; its
+// 128-row tiles would be 1/32 to 1/8 full.
+#pragma once
+
+#include "attn_tc.cuh"
+
+namespace serq {
+namespace attn {
+
+constexpr int kDecThreads = 288;
+constexpr int kBlockKeys = 64;
+
+struct DecArgs {
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  long long ldq, ldo;
+  float c;      // |scale| log2 e
+  float sign;   // of scale
+  int n_heads, group, row_blocks;  // row_blocks: 16-head blocks per kv head
+  int rows;     // rows per workspace slot, min(group, 16)
+  int prefix;   // keys in front that the shared-prefix pass has done
+  int shares;   // G
+  float* so;    // slots [2 G (+ batch x blocks of heads when prefix)][rows][D], normalised
+  float* slse;  // [slot][rows]
+  const float* po;    // prefix partials [split][batch][n_heads][D]
+  const float* plse;
+  int psplits;
+  BatchArgs b;
+  CacheArgs c_;
+};
+
+template <int D>
+struct DecLayout {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kOperand = kBlockKeys * D * 2;  // bytes of a block's K or V
+  static constexpr int kSlots = D == 128 ? 6 : 12;     // even: a slot is always the same warps'
+  static constexpr int oRing = 0;
+  static constexpr int oMerge = kSlots * 2 * kOperand;  // [4][16][D] floats, rows turned by 8 columns each
+  static constexpr int oStat = oMerge + 4 * 16 * D * 4;  // m and l: [2][8][16] floats
+  static constexpr int oBar = oStat + 2 * 8 * 16 * 4;
+  static constexpr int oMisc = oBar + 2 * kSlots * 8;
+  static constexpr int kAlloc = oMisc + 16 + 1024;
+  static_assert(kAlloc <= 232448, "shared memory of a CTA");
+};
+
+// Blocks of sequence b behind the prefix.
+__device__ __forceinline__ int dec_blocks(const DecArgs& a, int b) {
+  const int cap = a.b.max_pages << a.c_.page_shift;
+  return ceil_div(max(0, min(a.b.kv_len[b], cap) - a.prefix), kBlockKeys);
+}
+
+// Sum of the sequences' blocks, all of them and those before b (the warp calls).
+__device__ __forceinline__ void dec_sums(const DecArgs& a, int b, int lane, long long& before, long long& total) {
+  long long lo = 0, all = 0;
+  for (int i = lane; i < a.b.batch; i += 32) {
+    const int n = dec_blocks(a, i);
+    all += n;
+    if (i < b) lo += n;
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    lo += __shfl_xor_sync(0xffffffffu, lo, d);
+    all += __shfl_xor_sync(0xffffffffu, all, d);
+  }
+  before = lo;
+  total = all;
+}
+
+// Position in the batch's run of blocks.
+struct DecPos {
+  int b, h, blk, nb;  // sequence, head block, next block, blocks of the sequence
+};
+
+// The place of block w (the warp calls).  w < total * heads.
+__device__ __forceinline__ DecPos dec_find(const DecArgs& a, long long w, int heads, int lane) {
+  long long done = 0;
+  for (int b0 = 0; b0 < a.b.batch; b0 += 32) {
+    const int b = b0 + lane;
+    const int nb = b < a.b.batch ? dec_blocks(a, b) : 0;
+    long long incl = nb;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, w < (done + incl) * heads);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      DecPos p;
+      p.b = b0 + src;
+      p.nb = __shfl_sync(0xffffffffu, nb, src);
+      const long long rest = w - (done + __shfl_sync(0xffffffffu, incl, src) - p.nb) * heads;
+      p.h = (int)(rest / p.nb);
+      p.blk = (int)(rest - (long long)p.h * p.nb);
+      return p;
+    }
+    done += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return DecPos{0, 0, 0, 1};
+}
+
+__device__ __forceinline__ void dec_next_pair(const DecArgs& a, DecPos& p, int heads) {
+  p.blk = 0;
+  if (++p.h == heads) {
+    p.h = 0;
+    do {
+      ++p.b;
+      p.nb = p.b < a.b.batch ? dec_blocks(a, p.b) : 1;
+    } while (p.nb == 0);
+  }
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+      "%2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return reinterpret_cast<const uint32_t&>(h);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kDecThreads, 1)
+    k_decode_attn(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const DecArgs a) {
+  using L = DecLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::oBar);
+  uint64_t* empty = full + L::kSlots;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::oMisc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kSlots; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dep_wait();
+
+  const int heads = a.c_.n_kv_heads * a.row_blocks;
+  long long before, total;
+  dec_sums(a, 0, lane, before, total);
+  total *= heads;
+  const long long w0 = total * blockIdx.x / a.shares, w1 = total * (blockIdx.x + 1) / a.shares;
+  const int cap = a.b.max_pages << a.c_.page_shift;
+  DecPos p = {};
+  if (w0 < w1) p = dec_find(a, w0, heads, lane);
+
+  if (warp == 8) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    const int page = 1 << a.c_.page_shift;
+    const int box = min(page, kBlockKeys);
+    const int copies = kBlockKeys / box * L::kHalves;  // per operand
+    const int half = lane & (L::kHalves - 1), r = (lane / L::kHalves) * box;
+    // page of this lane's copy in the block at position p
+    auto lookup = [&](const DecPos& at) {
+      const int key = a.prefix + at.blk * kBlockKeys + r;
+      int pg = a.c_.n_pages;  // outside the map: filled with zeros
+      if (lane < copies && key < min(a.b.kv_len[at.b], cap)) {
+        const int e = a.b.table[(long long)at.b * a.b.ldt + (key >> a.c_.page_shift)];
+        if (e >= 0 && e < a.c_.n_pages) pg = e;
+        else note_bad_page();
+      }
+      return pg;
+    };
+    int pg = w0 < w1 ? lookup(p) : 0;
+    uint32_t slot = 0, ph = 0;
+    for (long long w = w0; w < w1; ++w) {
+      const DecPos cur = p;
+      const int cur_pg = pg;
+      if (++p.blk == p.nb) dec_next_pair(a, p, heads);
+      if (w + 1 < w1) pg = lookup(p);  // one block ahead of its copy
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ph ^ 1, abort_flag, kDevTimeoutProducer))) break;
+      if (lane == 0) mbar_arrive_expect_tx(&full[slot], 2 * L::kOperand);
+      __syncwarp();
+      if (lane < copies) {
+        const int key = a.prefix + cur.blk * kBlockKeys + r;
+        const int y = ((cur.h / a.row_blocks) << a.c_.page_shift) + (key & (page - 1));
+        uint8_t* dst = smem + L::oRing + slot * 2 * L::kOperand + half * (kBlockKeys * 128) + r * 128;
+        tma_load_3d(dst, &tmK, &full[slot], 64 * half, y, cur_pg);
+        tma_load_3d(dst + L::kOperand, &tmV, &full[slot], 64 * half, y, cur_pg);
+      }
+      __syncwarp();
+      if (++slot == L::kSlots) slot = 0, ph ^= 1;
+    }
+  } else {
+    const int wg = warp >> 2, kq = (warp & 3) * 16;  // this warp's keys of a block
+    const int quad = lane >> 2, qc = (lane & 3) * 2;
+    bool ok = true;
+    float* merge = reinterpret_cast<float*>(smem + L::oMerge);
+    float* st_m = reinterpret_cast<float*>(smem + L::oStat);
+    float* st_l = st_m + 8 * 16;
+    uint32_t it = 0;  // blocks since the share's first
+    for (long long w = w0; w < w1;) {
+      const int n = (int)min((long long)(p.nb - p.blk), w1 - w);
+      const int kvh = p.h / a.row_blocks, rb = p.h - kvh * a.row_blocks;
+      const int nrows = min(16, a.group - 16 * rb);
+      const int head0 = kvh * a.group + 16 * rb;
+      const int kv = min(a.b.kv_len[p.b], cap);
+      if (threadIdx.x == 0 && a.b.kv_len[p.b] > cap) note_bad_page();
+      uint32_t qf[D / 16][4];
+      {
+        const __nv_bfloat16* q0 = a.q + p.b * a.ldq + (long long)(head0 + quad) * D + qc;
+        const __nv_bfloat16* q1 = q0 + 8 * D;
+        const bool v0 = quad < nrows, v1 = quad + 8 < nrows;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          qf[k][0] = v0 ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k) : 0u;
+          qf[k][1] = v1 ? *reinterpret_cast<const uint32_t*>(q1 + 16 * k) : 0u;
+          qf[k][2] = v0 ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k + 8) : 0u;
+          qf[k][3] = v1 ? *reinterpret_cast<const uint32_t*>(q1 + 16 * k + 8) : 0u;
+        }
+      }
+      float o[D / 8][4] = {};
+      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // rows quad and quad + 8
+      for (int i = 0; i < n; ++i, ++it) {
+        if ((int)(it & 1) != wg) continue;
+        const uint32_t slot = it % L::kSlots, ph = (it / L::kSlots) & 1;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[slot], ph, abort_flag, kDevTimeoutEpilogue));
+        if (!ok) continue;
+        const uint32_t kb = smem_u32(smem + L::oRing + slot * 2 * L::kOperand), vb = kb + L::kOperand;
+        const int key0 = a.prefix + (p.blk + i) * kBlockKeys + kq;  // first key of this warp
+        if (key0 < kv) {
+          float s[2][4] = {};
+          {
+            const int r = kq + ((lane >> 4) << 3) + (lane & 7), cb = (lane >> 3) & 1;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              uint32_t f[4];
+              const int ch = (k & 3) * 2 + cb;
+              ldsm_x4(kb + (k >> 2) * (kBlockKeys * 128) + r * 128 + ((ch ^ (r & 7)) << 4), f);
+              mma_bf16(s[0], qf[k], f[0], f[1]);
+              mma_bf16(s[1], qf[k], f[2], f[3]);
+            }
+          }
+          const bool partial = key0 + 16 > kv;
+          uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;  // which of this thread's values exist
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][e] *= a.sign;
+          if (partial) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (key0 + 8 * t + qc + (e & 1) >= kv) s[t][e] = -INFINITY;
+            vm0 = (key0 + qc < kv ? 0xffffu : 0u) | (key0 + qc + 1 < kv ? 0xffff0000u : 0u);
+            vm1 = (key0 + 8 + qc < kv ? 0xffffu : 0u) | (key0 + 8 + qc + 1 < kv ? 0xffff0000u : 0u);
+          }
+          float c0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+          float c1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+#pragma unroll
+          for (int d = 1; d < 4; d <<= 1) {
+            c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, d));
+            c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, d));
+          }
+          c0 *= a.c;
+          c1 *= a.c;
+          const bool g0 = c0 > m0 + kLazyMax, g1 = c1 > m1 + kLazyMax;
+          if (__any_sync(0xffffffffu, g0 || g1)) {
+            const float f0 = g0 ? ex2(m0 - c0) : 1.f, f1 = g1 ? ex2(m1 - c1) : 1.f;
+            if (g0) m0 = c0;
+            if (g1) m1 = c1;
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll
+            for (int t = 0; t < D / 8; ++t) {
+              o[t][0] *= f0;
+              o[t][1] *= f0;
+              o[t][2] *= f1;
+              o[t][3] *= f1;
+            }
+          }
+          const float b0 = m0 == -INFINITY ? 0.f : -m0, b1 = m1 == -INFINITY ? 0.f : -m1;
+          float e[2][4];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            e[t][0] = ex2(fmaf(s[t][0], a.c, b0));
+            e[t][1] = ex2(fmaf(s[t][1], a.c, b0));
+            e[t][2] = ex2(fmaf(s[t][2], a.c, b1));
+            e[t][3] = ex2(fmaf(s[t][3], a.c, b1));
+          }
+          l0 += (e[0][0] + e[0][1]) + (e[1][0] + e[1][1]);
+          l1 += (e[0][2] + e[0][3]) + (e[1][2] + e[1][3]);
+          const uint32_t pf[4] = {pack_bf16(e[0][0], e[0][1]), pack_bf16(e[0][2], e[0][3]),
+                                  pack_bf16(e[1][0], e[1][1]), pack_bf16(e[1][2], e[1][3])};
+          const int r = kq + (((lane >> 3) & 1) << 3) + (lane & 7), cb = lane >> 4;
+#pragma unroll
+          for (int t = 0; t < D / 16; ++t) {
+            uint32_t f[4];
+            const int ch = (t & 3) * 2 + cb;
+            ldsm_x4_t(vb + (t >> 2) * (kBlockKeys * 128) + r * 128 + ((ch ^ (r & 7)) << 4), f);
+            if (partial) {  // values that do not exist may be NaN
+              f[0] &= vm0;
+              f[1] &= vm1;
+              f[2] &= vm0;
+              f[3] &= vm1;
+            }
+            mma_bf16(o[2 * t], pf, f[0], f[1]);
+            mma_bf16(o[2 * t + 1], pf, f[2], f[3]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);
+      }
+      // ------------------------------------------------- join the eight warps
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+      }
+      if ((lane & 3) == 0) {
+        st_m[warp * 16 + quad] = m0;
+        st_m[warp * 16 + quad + 8] = m1;
+        st_l[warp * 16 + quad] = l0;
+        st_l[warp * 16 + quad + 8] = l1;
+      }
+      auto sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+      sync();
+      float M0 = -INFINITY, M1 = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < 8; ++v) {
+        M0 = fmaxf(M0, st_m[v * 16 + quad]);
+        M1 = fmaxf(M1, st_m[v * 16 + quad + 8]);
+      }
+      const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M1);
+      auto slice = [&](int v, int row, int col) { return merge + (v * 16 + row) * D + ((col + 8 * row) & (D - 1)); };
+      const int v4 = warp & 3;
+      if (wg == 1) {
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t) {
+          if (quad < nrows)
+            *reinterpret_cast<float2*>(slice(v4, quad, 8 * t + qc)) = make_float2(o[t][0] * f0, o[t][1] * f0);
+          if (quad + 8 < nrows)
+            *reinterpret_cast<float2*>(slice(v4, quad + 8, 8 * t + qc)) =
+                make_float2(o[t][2] * f1, o[t][3] * f1);
+        }
+      }
+      sync();
+      if (wg == 0) {
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t) {
+          if (quad < nrows) {
+            float2* at = reinterpret_cast<float2*>(slice(v4, quad, 8 * t + qc));
+            *at = make_float2(at->x + o[t][0] * f0, at->y + o[t][1] * f0);
+          }
+          if (quad + 8 < nrows) {
+            float2* at = reinterpret_cast<float2*>(slice(v4, quad + 8, 8 * t + qc));
+            *at = make_float2(at->x + o[t][2] * f1, at->y + o[t][3] * f1);
+          }
+        }
+      }
+      sync();
+      // where the segment goes: whole pairs to O, or (with a prefix to join) to
+      // the pair's slot; a partial first segment to slot 2c, a partial last one
+      // to 2c + 1
+      const bool starts = p.blk == 0, ends = p.blk + n == p.nb;
+      const long long slot = !starts ? 2 * (long long)blockIdx.x
+                             : !ends ? 2 * (long long)blockIdx.x + 1
+                                     : 2 * (long long)a.shares + (long long)p.b * heads + p.h;
+      const bool final = starts && ends && a.prefix == 0;
+      for (int e = threadIdx.x; e < nrows * (D / 4); e += 256) {
+        const int row = e / (D / 4), c4 = (e - row * (D / 4)) * 4;
+        float mm = -INFINITY, z = 0.f;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) mm = fmaxf(mm, st_m[v * 16 + row]);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const float mv = st_m[v * 16 + row];
+          if (mv != -INFINITY) z += st_l[v * 16 + row] * ex2(mv - mm);
+        }
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float4 y = *reinterpret_cast<const float4*>(slice(v, row, c4));
+          x.x += y.x;
+          x.y += y.y;
+          x.z += y.z;
+          x.w += y.w;
+        }
+        const float inv = z > 0.f ? 1.f / z : 0.f;
+        x.x *= inv;
+        x.y *= inv;
+        x.z *= inv;
+        x.w *= inv;
+        if (!ok) continue;
+        if (final) {
+          *reinterpret_cast<uint2*>(a.o + p.b * a.ldo + (long long)(head0 + row) * D + c4) =
+              make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+        } else {
+          *reinterpret_cast<float4*>(a.so + (slot * a.rows + row) * D + c4) = x;
+          if (c4 == 0) a.slse[slot * a.rows + row] = z > 0.f ? mm + log2f(z) : -INFINITY;
+        }
+      }
+      sync();  // the buffers may be written again
+      w += n;
+      p.blk += n - 1;
+      if (++p.blk == p.nb) dec_next_pair(a, p, heads);
+    }
+  }
+  __syncthreads();
+  if (*abort_flag) {
+    if (threadIdx.x == 0) {
+      // let copies already issued land before the shared memory is released
+      const unsigned long long t0 = global_ns();
+      while (global_ns() - t0 < 100000ull) {
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins what k_decode_attn left in slots, and the shared prefix's partials:
+// O = sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M), in share order.  One CTA
+// per sequence and 8 heads, one warp per head.  A sequence without keys gets
+// zeros.
+template <int D>
+__global__ void __launch_bounds__(256) k_join(const DecArgs a) {
+  const int lane = threadIdx.x & 31, b = blockIdx.x;
+  const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
+  grid_dep_wait();
+  if (h >= a.n_heads) return;
+  const int heads = a.c_.n_kv_heads * a.row_blocks;
+  long long before, total;
+  dec_sums(a, b, lane, before, total);
+  total *= heads;
+  const int kvh = h / a.group, hr = h - kvh * a.group;
+  const int hb = kvh * a.row_blocks + hr / 16, row = hr & 15;
+  const int nb = dec_blocks(a, b);
+  const long long s0 = before * heads + (long long)hb * nb, s1 = s0 + nb;
+  // shares that hold the pair's first and last block
+  int c0 = 0, c1 = -1;
+  if (nb > 0) {
+    c0 = (int)(((s0 + 1) * a.shares - 1) / total);  // largest c with total c / shares <= s0
+    c1 = (int)((s1 * a.shares - 1) / total);
+    if (c0 == c1 && a.prefix == 0) return;  // finished by its CTA
+  }
+  constexpr int E = D / 32;
+  float acc[E] = {}, z = 0.f, m = -INFINITY;
+  auto add = [&](float lse, const float* src) {
+    if (lse == -INFINITY) return;
+    const float mn = fmaxf(m, lse), f = ex2(m - mn), w = ex2(lse - mn);
+    m = mn;
+    z = z * f + w;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + w * src[lane * E + e];
+  };
+  for (int s = 0; s < (a.prefix ? a.psplits : 0); ++s) {
+    const long long at = ((long long)s * a.b.batch + b) * a.n_heads + h;
+    add(a.plse[at], a.po + at * D);
+  }
+  for (int c = c0; c <= c1; ++c) {
+    const long long w0 = total * c / a.shares, w1 = total * (c + 1) / a.shares;
+    if (w0 == w1) continue;  // fewer blocks than shares
+    const bool starts = w0 <= s0, ends = w1 >= s1;
+    const long long slot = !starts ? 2ll * c : !ends ? 2ll * c + 1 : 2ll * a.shares + (long long)b * heads + hb;
+    add(a.slse[slot * a.rows + row], a.so + (slot * a.rows + row) * D);
+  }
+  const float inv = z > 0.f ? 1.f / z : 0.f;
+  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + b * a.ldo + (long long)h * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) dst[e] = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+}
+
+template <int D>
+inline cudaError_t launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV, const DecArgs& a, cudaStream_t st) {
+  auto kern = k_decode_attn<D>;
+  cudaError_t e = smem_limit(reinterpret_cast<const void*>(kern), DecLayout<D>::kAlloc);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.shares);
+  cfg.blockDim = dim3(kDecThreads);
+  cfg.dynamicSmemBytes = DecLayout<D>::kAlloc;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(a.b.batch, (a.n_heads + 7) / 8);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, k_join<D>, a);
+}
+
+}  // namespace attn
+}  // namespace serq

@@ -23,7 +23,7 @@
 
 #include <algorithm>
 
-#include "attn.cuh"
+#include "rope.cuh"
 
 namespace serq {
 namespace attn {

@@ -24,8 +24,8 @@
 #include "quant.cuh"
 #include "mxfp4.cuh"
 #include "rope.cuh"
-#include "attn.cuh"
 #include "attn_tc.cuh"
+#include "attn_decode.cuh"
 
 namespace {
 
@@ -1771,7 +1771,7 @@ struct serq_kv_cache {
   int n_pages, page_size, page_shift, n_kv_heads, head_dim, device;
   int64_t page_stride;
   __nv_bfloat16 *K, *V;
-  CUtensorMap tmK, tmV;  // box: 64 elements x min(page_size, 128) slots of one head
+  CUtensorMap tm[2][2];  // K, V; box: 64 elements x min(page_size, 128 | 64) slots of one head
 };
 
 namespace {
@@ -1936,10 +1936,10 @@ serq_status serq_kv_cache_create(void* K, void* V, int n_pages, int page_size, i
   c->K = static_cast<__nv_bfloat16*>(K);
   c->V = static_cast<__nv_bfloat16*>(V);
   cudaGetDevice(&c->device);
-  const uint32_t box = page_size < 128 ? page_size : 128;
-  for (int i = 0; i < 2; ++i)
-    if (!make_map_bf16_3d(i ? &c->tmV : &c->tmK, i ? V : K, head_dim, (uint64_t)n_kv_heads * page_size, n_pages,
-                          (uint64_t)head_dim * 2, (uint64_t)page_stride * 2, box, 1)) {
+  for (int i = 0; i < 4; ++i)
+    if (!make_map_bf16_3d(&c->tm[i & 1][i >> 1], i & 1 ? V : K, head_dim, (uint64_t)n_kv_heads * page_size, n_pages,
+                          (uint64_t)head_dim * 2, (uint64_t)page_stride * 2, std::min(page_size, i < 2 ? 128 : 64),
+                          1)) {
       delete c;
       return fail(SERQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
     }
@@ -2000,11 +2000,6 @@ serq_status serq_rope_append(const serq_rope* rope, const serq_kv_cache* cache, 
   return ok();
 }
 
-size_t serq_attn_decode_ws_bytes(const serq_kv_cache* cache, int batch, int n_heads, int max_pages, int prefix_len,
-                                 int max_kv) {
-  return 0;
-}
-
 }  // extern "C"
 
 namespace {
@@ -2012,26 +2007,6 @@ namespace {
 // |scale| log2 e; a zero scale becomes the smallest normal number, so that a
 // masked score stays -inf instead of turning into a NaN.
 float attn_scale(float scale) { return std::max(std::fabs(scale) * 1.4426950408889634f, 1.17549435e-38f); }
-
-serq_status attn_rows(const serq_kv_cache* c, const void* Q, int ldq, int T, int n_heads, float scale, int batch,
-                      const int32_t* cu_q, const int32_t* kv_len, const int32_t* table, int max_pages, int ld_table,
-                      int prefix, void* O, int ldo, void* stream, const char* what) {
-  serq::attn::Args a;
-  a.q = static_cast<const __nv_bfloat16*>(Q);
-  a.o = static_cast<__nv_bfloat16*>(O);
-  a.ldq = ldq;
-  a.ldo = ldo;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.T = T;
-  a.n_heads = n_heads;
-  a.prefix = prefix;
-  a.b = {cu_q, kv_len, table, batch, max_pages, ld_table};
-  a.c = cache_args(c);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = c->head_dim == 128 ? serq::attn::launch_rows<128>(a, st) : serq::attn::launch_rows<64>(a, st);
-  if (e != cudaSuccess) return cuda_fail(e, what);
-  return ok();
-}
 
 serq_status check_attn(const serq_kv_cache* c, const void* Q, int ldq, int n_heads, float scale, int batch,
                        const int32_t* kv_len, const int32_t* table, int max_pages, int ld_table, int max_kv,
@@ -2122,13 +2097,55 @@ serq_status serq_attn_prefill(const serq_kv_cache* cache, const void* Q, int ldq
   a.c_ = cache_args(cache);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const long long items = p.pairs * cache->n_kv_heads * p.splits;
-  cudaError_t e = D == 128 ? serq::attn::launch_tc<128>(tmQ, cache->tmK, cache->tmV, a, items, sm_count(), st)
-                           : serq::attn::launch_tc<64>(tmQ, cache->tmK, cache->tmV, a, items, sm_count(), st);
+  cudaError_t e = D == 128 ? serq::attn::launch_tc<128>(tmQ, cache->tm[0][0], cache->tm[1][0], a, items, sm_count(), st)
+                           : serq::attn::launch_tc<64>(tmQ, cache->tm[0][0], cache->tm[1][0], a, items, sm_count(), st);
   if (e == cudaSuccess && p.ws)
     e = D == 128 ? serq::attn::launch_merge<128>(a.po, a.plse, p.splits, T, n_heads, cu_q, batch, a.o, ldo, st)
                  : serq::attn::launch_merge<64>(a.po, a.plse, p.splits, T, n_heads, cu_q, batch, a.o, ldo, st);
   if (e != cudaSuccess) return cuda_fail(e, "serq_attn_prefill launch");
   return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
+// Work split and workspace of a decode call.
+struct DecodePlan {
+  int group, row_blocks, rows, shares;
+  int prefix, tokens, psplits;  // the shared prefix's pass, when prefix > 0
+  long long pairs;
+  size_t slots, ws;
+};
+DecodePlan decode_plan(const serq_kv_cache* c, int batch, int n_heads, int max_pages, int prefix_len, int max_kv) {
+  DecodePlan p = {};
+  p.group = n_heads / c->n_kv_heads;
+  p.row_blocks = (p.group + 15) / 16;
+  p.rows = std::min(p.group, 16);
+  p.prefix = batch > 1 ? prefix_len : 0;  // one sequence shares with nobody
+  const long long cap = (long long)max_pages * c->page_size;
+  const long long keys = std::max(0ll, (max_kv ? std::min<long long>(max_kv, cap) : cap) - p.prefix);
+  const long long blocks = (keys + serq::attn::kBlockKeys - 1) / serq::attn::kBlockKeys * batch * c->n_kv_heads * p.row_blocks;
+  p.shares = (int)std::max(1ll, std::min<long long>(blocks, sm_count()));
+  p.slots = 2 * (size_t)p.shares;
+  if (p.prefix) {
+    p.slots += (size_t)batch * c->n_kv_heads * p.row_blocks;
+    p.tokens = serq::attn::kTileRows / p.group;
+    p.pairs = (batch + 2 * p.tokens - 1) / (2 * p.tokens);
+    p.psplits = serq::attn::tc_splits(p.pairs, c->n_kv_heads, p.prefix, sm_count());
+  }
+  p.ws = (p.slots * p.rows + (size_t)p.psplits * batch * n_heads) * (c->head_dim + 1) * sizeof(float);
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t serq_attn_decode_ws_bytes(const serq_kv_cache* cache, int batch, int n_heads, int max_pages, int prefix_len,
+                                 int max_kv) {
+  if (!cache || batch < 1 || max_pages < 1 || prefix_len < 0 || max_kv < 0 || check_heads(cache, n_heads)) return 0;
+  return decode_plan(cache, batch, n_heads, max_pages, prefix_len, max_kv).ws;
 }
 
 serq_status serq_attn_decode(const serq_kv_cache* cache, const void* Q, int ldq, int n_heads, float scale, int batch,
@@ -2143,8 +2160,60 @@ serq_status serq_attn_decode(const serq_kv_cache* cache, const void* Q, int ldq,
     return s;
   if ((s = check_device())) return s;
   if ((s = check_handle_device(cache->device, "the cache"))) return s;
-  return attn_rows(cache, Q, ldq, batch, n_heads, scale, batch, nullptr, kv_len, page_table, max_pages, ld_table, prefix_len,
-                   O, ldo, stream, "serq_attn_decode launch");
+  const int D = cache->head_dim;
+  const DecodePlan p = decode_plan(cache, batch, n_heads, max_pages, prefix_len, max_kv);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  serq::attn::DecArgs d;
+  d.q = static_cast<const __nv_bfloat16*>(Q);
+  d.o = static_cast<__nv_bfloat16*>(O);
+  d.ldq = ldq;
+  d.ldo = ldo;
+  d.c = attn_scale(scale);
+  d.sign = scale < 0.f ? -1.f : 1.f;
+  d.n_heads = n_heads;
+  d.group = p.group;
+  d.row_blocks = p.row_blocks;
+  d.rows = p.rows;
+  d.prefix = p.prefix;
+  d.shares = p.shares;
+  d.b = {nullptr, kv_len, page_table, batch, max_pages, ld_table};
+  d.c_ = cache_args(cache);
+  // workspace: slot outputs, prefix outputs, then the log-sums of both
+  const size_t n_slot = p.slots * p.rows, n_pre = (size_t)p.psplits * batch * n_heads;
+  d.so = static_cast<float*>(ws);
+  float* po = d.so + n_slot * D;
+  d.slse = po + n_pre * D;
+  float* plse = d.slse + n_slot;
+  d.po = po;
+  d.plse = plse;
+  d.psplits = p.psplits;
+  cudaError_t e = cudaSuccess;
+  if (p.prefix) {
+    CUtensorMap tmQ;
+    if (!map_rows(&tmQ, Q, ldq, batch, n_heads, D, p.group, p.tokens))
+      return fail(SERQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for Q");
+    serq::attn::TcArgs a = {};
+    a.po = po;
+    a.plse = plse;
+    a.c = d.c;
+    a.neg = scale < 0.f;
+    a.T = batch;
+    a.n_heads = n_heads;
+    a.group = p.group;
+    a.tokens = p.tokens;
+    a.splits = p.psplits;
+    a.prefix = p.prefix;
+    a.b = d.b;
+    a.c_ = d.c_;
+    const long long items = p.pairs * cache->n_kv_heads * p.psplits;
+    e = D == 128 ? serq::attn::launch_tc<128>(tmQ, cache->tm[0][0], cache->tm[1][0], a, items, sm_count(), st)
+                 : serq::attn::launch_tc<64>(tmQ, cache->tm[0][0], cache->tm[1][0], a, items, sm_count(), st);
+  }
+  if (e == cudaSuccess)
+    e = D == 128 ? serq::attn::launch_decode<128>(cache->tm[0][1], cache->tm[1][1], d, st)
+                 : serq::attn::launch_decode<64>(cache->tm[0][1], cache->tm[1][1], d, st);
+  if (e != cudaSuccess) return cuda_fail(e, "serq_attn_decode launch");
+  return ok();
 }
 
 }  // extern "C"
