@@ -168,7 +168,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     fence_mbar_init();
   }
   __syncthreads();
-  grid_dep_wait();
+  // Behind the shared-prefix pass of the same call (which has waited for
+  // whatever came before it) there is nothing to wait for until the end.
+  if (a.prefix == 0) grid_dep_wait();
+  grid_dep_launch();
 
   const int heads = a.c_.n_kv_heads * a.row_blocks;
   long long before, total;
@@ -435,6 +438,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       if (++p.blk == p.nb) dec_next_pair(a, p, heads);
     }
   }
+  if (a.prefix != 0) grid_dep_wait();  // k_join waits for this grid only
   __syncthreads();
   if (*abort_flag) {
     if (threadIdx.x == 0) {
@@ -448,15 +452,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 }
 
 // Joins what k_decode_attn left in slots, and the shared prefix's partials:
-// O = sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M), in share order.  One CTA
-// per sequence and 8 heads, one warp per head.  A sequence without keys gets
-// zeros.
+// O = sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M).  One CTA per sequence and
+// head; its four warps take every fourth part and add up in a fixed order.  A
+// sequence without keys gets zeros.
 template <int D>
-__global__ void __launch_bounds__(256) k_join(const DecArgs a) {
-  const int lane = threadIdx.x & 31, b = blockIdx.x;
-  const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
-  grid_dep_wait();
-  if (h >= a.n_heads) return;
+__global__ void __launch_bounds__(128) k_join(const DecArgs a) {
+  __shared__ float part[4][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.x, b = blockIdx.y;
+  // the lengths are inputs of the call: k_decode_attn lets this grid start
+  // only after its own wait, so they are complete here
   const int heads = a.c_.n_kv_heads * a.row_blocks;
   long long before, total;
   dec_sums(a, b, lane, before, total);
@@ -468,35 +472,69 @@ __global__ void __launch_bounds__(256) k_join(const DecArgs a) {
   // shares that hold the pair's first and last block
   int c0 = 0, c1 = -1;
   if (nb > 0) {
-    c0 = (int)(((s0 + 1) * a.shares - 1) / total);  // largest c with total c / shares <= s0
+    c0 = (int)(((s0 + 1) * a.shares - 1) / total);  // largest c with floor(total c / shares) <= s0
     c1 = (int)((s1 * a.shares - 1) / total);
-    if (c0 == c1 && a.prefix == 0) return;  // finished by its CTA
   }
-  constexpr int E = D / 32;
-  float acc[E] = {}, z = 0.f, m = -INFINITY;
-  auto add = [&](float lse, const float* src) {
-    if (lse == -INFINITY) return;
-    const float mn = fmaxf(m, lse), f = ex2(m - mn), w = ex2(lse - mn);
-    m = mn;
-    z = z * f + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + w * src[lane * E + e];
+  grid_dep_wait();
+  if (nb > 0 && c0 == c1 && a.prefix == 0) return;  // finished by its CTA
+  const int np = a.prefix ? a.psplits : 0, n = np + c1 - c0 + 1;
+  // part i: log-sum and place of its row (in rows of D floats)
+  auto find = [&](int i, const float*& src) {
+    float lse = -INFINITY;
+    if (i < np) {
+      const long long at = ((long long)i * a.b.batch + b) * a.n_heads + h;
+      lse = a.plse[at];
+      src = a.po + at * D;
+    } else if (i < n) {
+      const long long c = c0 + i - np, w0 = total * c / a.shares, w1 = total * (c + 1) / a.shares;
+      if (w0 < w1) {  // else: fewer blocks than shares
+        const long long slot = w0 > s0   ? 2 * c
+                               : w1 < s1 ? 2 * c + 1
+                                         : 2ll * a.shares + (long long)b * heads + hb;
+        lse = a.slse[slot * a.rows + row];
+        src = a.so + (slot * a.rows + row) * D;
+      }
+    }
+    return lse;
   };
-  for (int s = 0; s < (a.prefix ? a.psplits : 0); ++s) {
-    const long long at = ((long long)s * a.b.batch + b) * a.n_heads + h;
-    add(a.plse[at], a.po + at * D);
+  constexpr int E = D / 32;
+  const float* src = a.so;
+  float lse = find(lane, src), m = lse;
+  for (int i = 32 + lane; i < n; i += 32) {
+    const float* unused;
+    m = fmaxf(m, find(i, unused));
   }
-  for (int c = c0; c <= c1; ++c) {
-    const long long w0 = total * c / a.shares, w1 = total * (c + 1) / a.shares;
-    if (w0 == w1) continue;  // fewer blocks than shares
-    const bool starts = w0 <= s0, ends = w1 >= s1;
-    const long long slot = !starts ? 2ll * c : !ends ? 2ll * c + 1 : 2ll * a.shares + (long long)b * heads + hb;
-    add(a.slse[slot * a.rows + row], a.so + (slot * a.rows + row) * D);
-  }
-  const float inv = z > 0.f ? 1.f / z : 0.f;
-  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + b * a.ldo + (long long)h * D + lane * E);
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e) dst[e] = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  float acc[E] = {}, z = 0.f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    if (i0) lse = find(i0 + lane, src);
+    const float w = lse == -INFINITY ? 0.f : ex2(lse - m);
+    z += w;
+    const int cnt = min(32, n - i0);
+#pragma unroll 4
+    for (int i = warp; i < cnt; i += 4) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* from = reinterpret_cast<const float*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
+      if (wi != 0.f) {  // an empty part's row is not written
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += wi * from[lane + 32 * e];
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+#pragma unroll
+  for (int e = 0; e < E; ++e) part[warp][lane + 32 * e] = acc[e];
+  __syncthreads();
+  const float inv = z > 0.f ? 1.f / z : 0.f;
+  const int e = threadIdx.x * 2;
+  if (e < D) {
+    const float x = (part[0][e] + part[1][e]) + (part[2][e] + part[3][e]);
+    const float y = (part[0][e + 1] + part[1][e + 1]) + (part[2][e + 1] + part[3][e + 1]);
+    *reinterpret_cast<uint32_t*>(a.o + b * a.ldo + (long long)h * D + e) = pack_bf16(x * inv, y * inv);
+  }
 }
 
 template <int D>
@@ -516,8 +554,8 @@ inline cudaError_t launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV,
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(a.b.batch, (a.n_heads + 7) / 8);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(a.n_heads, a.b.batch);
+  cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, k_join<D>, a);
 }

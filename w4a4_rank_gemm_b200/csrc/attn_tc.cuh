@@ -94,17 +94,18 @@ __device__ __forceinline__ void decode_item(const TcArgs& a, int w, int lane, It
   w /= a.c_.n_kv_heads;
   const int cap = a.b.max_pages << a.c_.page_shift;
   it.done = 0;
-  int seq = 0, tile = w, first = 0, n = 0;
+  int seq = 0, tile = w, first = 0, n = 0, kv = 0;
   if (a.prefix) {
     n = a.T;
     const int tiles = ceil_div(n, pair);
     if (w >= tiles) it.done = 1;
   } else {
     // the w-th tile pair from the back
-    int total = 0;
+    int total = 0, kv_mine = 0;
     for (int b0 = 0; b0 < a.b.batch; b0 += 32) {
       const int b = b0 + lane;
       const int nb = b < a.b.batch ? max(0, a.b.cu_q[b + 1] - a.b.cu_q[b]) : 0;
+      kv_mine = b < a.b.batch ? a.b.kv_len[b] : 0;  // read with the offsets, not after them
       total += __reduce_add_sync(0xffffffffu, ceil_div(nb, pair));
     }
     if (w >= total) {
@@ -114,6 +115,8 @@ __device__ __forceinline__ void decode_item(const TcArgs& a, int w, int lane, It
       for (int b0 = 0; b0 < a.b.batch; b0 += 32) {
         const int b = b0 + lane;
         const int nb = b < a.b.batch ? max(0, a.b.cu_q[b + 1] - a.b.cu_q[b]) : 0;
+        const int from = b < a.b.batch ? a.b.cu_q[b] : 0;
+        if (a.b.batch > 32) kv_mine = b < a.b.batch ? a.b.kv_len[b] : 0;
         const int mine = ceil_div(nb, pair);
         int incl = mine;
 #pragma unroll
@@ -128,11 +131,12 @@ __device__ __forceinline__ void decode_item(const TcArgs& a, int w, int lane, It
           seq = b0 + src;
           tile = left - (__shfl_sync(0xffffffffu, incl, src) - __shfl_sync(0xffffffffu, mine, src));
           n = __shfl_sync(0xffffffffu, nb, src);
+          first = __shfl_sync(0xffffffffu, from, src);
+          kv = __shfl_sync(0xffffffffu, kv_mine, src);
           break;
         }
         left -= sum;
       }
-      first = a.b.cu_q[seq];
     }
   }
   if (it.done) return;
@@ -146,7 +150,6 @@ __device__ __forceinline__ void decode_item(const TcArgs& a, int w, int lane, It
     it.lim0 = 0;
     limA = limB = it.kv_end;
   } else {
-    const int kv = a.b.kv_len[seq];
     it.kv_end = max(0, min(kv, cap));
     if (kv > cap && lane == 0) note_bad_page();
     it.lim0 = kv - n + tile * pair + 1;
@@ -227,6 +230,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tma_prefetch_desc(&tmV);
     }
     grid_dep_wait();
+    grid_dep_launch();
     const int page = 1 << a.c_.page_shift;
     const int box = min(page, kTileKeys);         // rows per copy
     const int copies = kTileKeys / box * L::kHalves;  // per step and operand
@@ -562,7 +566,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // Joins partial outputs: O = sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M).
-// One warp per (row, head); splits whose part is empty are not read.
+// One warp per (row, head); a lane holds one split's weight (splits <= 64).
 template <int D>
 __global__ void __launch_bounds__(128) k_merge(const float* po, const float* plse, int splits, int T, int n_heads,
                                                const int32_t* cu_q, int batch, __nv_bfloat16* o, long long ldo) {
@@ -572,19 +576,22 @@ __global__ void __launch_bounds__(128) k_merge(const float* po, const float* pls
   grid_dep_wait();
   if (r >= rows) return;
   const int t = (int)(r / n_heads), h = (int)(r % n_heads);
-  if (cu_q != nullptr && (t < cu_q[0] || t >= cu_q[batch])) return;
-  float m = -INFINITY;
-  for (int s = lane; s < splits; s += 32) m = fmaxf(m, plse[s * rows + r]);
+  const float ls0 = lane < splits ? plse[lane * rows + r] : -INFINITY;
+  const float ls1 = lane + 32 < splits ? plse[(lane + 32) * rows + r] : -INFINITY;
+  if (t < cu_q[0] || t >= cu_q[batch]) return;
+  float m = fmaxf(ls0, ls1);
 #pragma unroll
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float w0 = ls0 == -INFINITY ? 0.f : ex2(ls0 - m), w1 = ls1 == -INFINITY ? 0.f : ex2(ls1 - m);
+  float z = w0 + w1;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
   constexpr int E = D / 32;
-  float acc[E] = {}, z = 0.f;
-  if (m != -INFINITY) {
-    for (int s = 0; s < splits; ++s) {
-      const float ls = plse[s * rows + r];
-      if (ls == -INFINITY) continue;
-      const float w = ex2(ls - m);
-      z += w;
+  float acc[E] = {};
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const float w = __shfl_sync(0xffffffffu, s < 32 ? w0 : w1, s & 31);
+    if (w != 0.f) {  // an empty part's row is not written
       const float* src = po + (s * rows + r) * D + lane * E;
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] += w * src[e];

@@ -661,6 +661,8 @@ class KVCache:
         self.K, self.V = K, V
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = K.shape
         self.device = K.device
+        self.index = K.get_device()
+        self.default_scale = self.head_dim ** -0.5
         stride = K.stride(0) if self.n_pages > 1 else K[0].numel()
         h = _vp()
         with torch.cuda.device(self.device):
@@ -684,45 +686,63 @@ class KVCache:
             pass
 
 
-def _token_rows(t: torch.Tensor, name: str, cache: KVCache, heads: Optional[int] = None) -> int:
+def _token_rows(t: torch.Tensor, name: str, cache: KVCache, rows: Optional[int] = None, heads: Optional[int] = None):
     """Checks bf16 token rows of whole heads on the cache's device; returns
-    their number of heads."""
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.stride(1) != 1 or t.device != cache.device:
-        raise ValueError(f"{name} must be a 2-D bf16 tensor with unit column stride on the cache's device")
-    n = t.shape[1] // cache.head_dim
-    if n * cache.head_dim != t.shape[1] or (heads is not None and n != heads):
-        raise ValueError(f"{name} has {t.shape[1]} columns, not {'whole' if heads is None else heads} heads of "
-                         f"{cache.head_dim}")
-    return n
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+    rows, heads and row stride.  (These checks run once per tensor and call:
+    as few calls into torch as they can be written with.)"""
+    if t.dtype is not torch.bfloat16 or t.dim() != 2 or t.get_device() != cache.index:
+        raise ValueError(f"{name} must be a 2-D bf16 tensor on the cache's device")
+    n, cols = t.shape
+    ld, unit = t.stride()
+    h = cols // cache.head_dim
+    if unit != 1 or h * cache.head_dim != cols or h == 0 or (heads is not None and h != heads):
+        raise ValueError(f"{name} must hold {'whole' if heads is None else heads} heads of {cache.head_dim} with unit "
+                         f"column stride (its rows have {cols} columns)")
+    if rows is not None and n != rows:
+        raise ValueError(f"{name} has {n} rows, not {rows}")
+    return n, h, ld if n > 1 else cols
 
 
 def _batch_args(cache: KVCache, kv_len: torch.Tensor, page_table: torch.Tensor, cu_q: Optional[torch.Tensor] = None):
-    for t, n, d in ((kv_len, "kv_len", 1), (page_table, "page_table", 2), (cu_q, "cu_q", 1)):
-        if t is not None and (t.dtype != torch.int32 or t.dim() != d or t.stride(-1) != 1 or t.device != cache.device):
-            raise ValueError(f"{n} must be a {d}-D int32 tensor with unit stride on the cache's device")
+    i32, index = torch.int32, cache.index
+    if kv_len.dtype is not i32 or kv_len.dim() != 1 or kv_len.get_device() != index or not kv_len.is_contiguous():
+        raise ValueError("kv_len must be a dense 1-D int32 tensor on the cache's device")
     B = kv_len.shape[0]
-    if page_table.shape[0] != B or (cu_q is not None and cu_q.shape[0] != B + 1):
-        raise ValueError("page_table needs a row for each sequence, cu_q one entry more")
-    cols = page_table.shape[1]
-    return B, cols, page_table.stride(0) if B > 1 else cols
+    if page_table.dtype is not i32 or page_table.dim() != 2 or page_table.get_device() != index:
+        raise ValueError("page_table must be a 2-D int32 tensor on the cache's device")
+    n, cols = page_table.shape
+    ld, unit = page_table.stride()
+    if n != B or (unit != 1 and cols > 1):
+        raise ValueError("page_table needs a row with unit column stride for each sequence")
+    if cu_q is not None and (cu_q.dtype is not i32 or cu_q.dim() != 1 or cu_q.get_device() != index or
+                             cu_q.shape[0] != B + 1 or not cu_q.is_contiguous()):
+        raise ValueError("cu_q must be a dense 1-D int32 tensor of one entry more than sequences on the cache's device")
+    return B, cols, ld if B > 1 else cols
 
 
-def _on(cache: KVCache, stream):
-    """Device guard and stream of a call on the cache's device."""
-    return torch.cuda.device(cache.device), stream if stream is not None else torch.cuda.current_stream(cache.device)
+def _call(cache: KVCache, stream, where: str, f, *args):
+    """Runs f(*args, stream) with the cache's device current, on its current
+    stream unless one is given."""
+    st = torch._C._cuda_getCurrentRawStream(cache.index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == cache.index:
+        status = f(*args, st)
+    else:
+        with torch.cuda.device(cache.index):
+            status = f(*args, st)
+    if status != OK:
+        raise SerqError(status, where)
 
 
-def _scratch(n: int, cache: KVCache, ws: Optional[torch.Tensor], stream) -> Optional[torch.Tensor]:
-    if ws is None:
-        if n == 0:
-            return None
-        with torch.cuda.stream(stream):
-            return torch.empty(n, dtype=torch.uint8, device=cache.device)
-    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != cache.device:
+def _scratch(n: int, cache: KVCache, stream) -> Optional[torch.Tensor]:
+    """n bytes, in the order of the call's stream."""
+    if n == 0:
+        return None
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def _check_ws(ws: torch.Tensor, cache: KVCache) -> torch.Tensor:
+    if ws.dtype is not torch.uint8 or not ws.is_contiguous() or ws.get_device() != cache.index:
         raise ValueError("ws must be a contiguous uint8 tensor on the cache's device")
     return ws
 
@@ -738,46 +758,44 @@ def rope_append(rope: Rope, cache: KVCache, Q: torch.Tensor, K: torch.Tensor, V:
                 stream=None) -> torch.Tensor:
     """serq_rope_append: rotated (and normalised, when weights are given)
     queries are returned, rotated keys and the values go to the cache.  Q, K,
-    V are T x heads * head_dim rows; Qout may be Q."""
-    n_heads = _token_rows(Q, "Q", cache)
-    _token_rows(K, "K", cache, cache.n_kv_heads)
-    _token_rows(V, "V", cache, cache.n_kv_heads)
-    T = Q.shape[0]
-    if K.shape[0] != T or V.shape[0] != T:
-        raise ValueError("Q, K and V must have the same rows")
+    V are T x heads * head_dim rows; Qout may be Q.  Rows that hold no token
+    are left as they are in Qout (undefined where it is allocated here)."""
+    T, n_heads, ldq = _token_rows(Q, "Q", cache)
+    ldk = _token_rows(K, "K", cache, T, cache.n_kv_heads)[2]
+    ldv = _token_rows(V, "V", cache, T, cache.n_kv_heads)[2]
     for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != torch.bfloat16 or w.shape != (cache.head_dim,) or not w.is_contiguous()
-                              or w.device != cache.device):
+        if w is not None and (w.dtype is not torch.bfloat16 or w.shape != (cache.head_dim,) or not w.is_contiguous()
+                              or w.get_device() != cache.index):
             raise ValueError("norm weights must be contiguous bf16 tensors of head_dim elements")
     if cu_q is None:
         raise ValueError("cu_q is needed")
     B, cols, ldt = _batch_args(cache, kv_len, page_table, cu_q)
-    guard, st = _on(cache, stream)
-    with guard:
-        if Qout is None:
-            Qout = _out_like(Q, st)
-        elif _token_rows(Qout, "Qout", cache, n_heads) and Qout.shape[0] != T:
-            raise ValueError("Qout must have Q's rows")
-        _check(lib.serq_rope_append(rope.handle, cache.handle, _ptr(Q), _row_stride(Q), _ptr(K), _row_stride(K),
-                                    _ptr(V), _row_stride(V), T, n_heads, _ptr(q_weight), _ptr(k_weight), eps, B,
-                                    _ptr(cu_q), _ptr(kv_len), _ptr(page_table), cols, ldt, _ptr(Qout),
-                                    _row_stride(Qout), _vp(st.cuda_stream)), "serq_rope_append")
+    if Qout is None:
+        Qout = _out_like(Q, stream)
+    ldo = _token_rows(Qout, "Qout", cache, T, n_heads)[2]
+    _call(cache, stream, "serq_rope_append", lib.serq_rope_append, rope.handle, cache.handle, Q.data_ptr(), ldq,
+          K.data_ptr(), ldk, V.data_ptr(), ldv, T, n_heads, None if q_weight is None else q_weight.data_ptr(),
+          None if k_weight is None else k_weight.data_ptr(), eps, B, cu_q.data_ptr(), kv_len.data_ptr(),
+          page_table.data_ptr(), cols, ldt, Qout.data_ptr(), ldo)
     return Qout
+
+
+def _ws_bytes(cache: KVCache, f, *args) -> int:
+    with torch.cuda.device(cache.index):
+        return f(cache.handle, *args)
 
 
 def attn_prefill_ws(cache: KVCache, T: int, n_heads: int, batch: int, max_pages: int, max_kv: int = 0):
     """Scratch for attn_prefill calls of these sizes (None where none is
     needed); calls that may run at the same time need one each."""
-    with torch.cuda.device(cache.device):
-        n = lib.serq_attn_prefill_ws_bytes(cache.handle, T, n_heads, batch, max_pages, max_kv)
-    return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
+    n = _ws_bytes(cache, lib.serq_attn_prefill_ws_bytes, T, n_heads, batch, max_pages, max_kv)
+    return _scratch(n, cache, None)
 
 
 def attn_decode_ws(cache: KVCache, batch: int, n_heads: int, max_pages: int, prefix_len: int = 0, max_kv: int = 0):
     """The same for attn_decode."""
-    with torch.cuda.device(cache.device):
-        n = lib.serq_attn_decode_ws_bytes(cache.handle, batch, n_heads, max_pages, prefix_len, max_kv)
-    return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
+    n = _ws_bytes(cache, lib.serq_attn_decode_ws_bytes, batch, n_heads, max_pages, prefix_len, max_kv)
+    return _scratch(n, cache, None)
 
 
 def attn_prefill(cache: KVCache, Q: torch.Tensor, cu_q: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
@@ -785,24 +803,23 @@ def attn_prefill(cache: KVCache, Q: torch.Tensor, cu_q: torch.Tensor, kv_len: to
                  max_kv: int = 0, stream=None) -> torch.Tensor:
     """serq_attn_prefill: causal attention of the packed rows Q (T x heads *
     head_dim) over their sequences' cached keys; scale defaults to
-    1 / sqrt(head_dim)."""
-    n_heads = _token_rows(Q, "Q", cache)
+    1 / sqrt(head_dim), ws to scratch allocated here.  Rows outside the batch
+    are left as they are in O."""
+    T, n_heads, ldq = _token_rows(Q, "Q", cache)
     if cu_q is None:
         raise ValueError("cu_q is needed")
     B, cols, ldt = _batch_args(cache, kv_len, page_table, cu_q)
-    T = Q.shape[0]
-    guard, st = _on(cache, stream)
-    with guard:
-        if O is None:
-            O = _out_like(Q, st)
-        elif _token_rows(O, "O", cache, n_heads) and O.shape[0] != T:
-            raise ValueError("O must have Q's rows")
-        ws = _scratch(lib.serq_attn_prefill_ws_bytes(cache.handle, T, n_heads, B, cols, max_kv) if ws is None else 0,
-                      cache, ws, st)
-        _check(lib.serq_attn_prefill(cache.handle, _ptr(Q), _row_stride(Q), T, n_heads,
-                                     cache.head_dim ** -0.5 if scale is None else scale, B, _ptr(cu_q), _ptr(kv_len),
-                                     _ptr(page_table), cols, ldt, max_kv, _ptr(ws), 0 if ws is None else ws.numel(),
-                                     _ptr(O), _row_stride(O), _vp(st.cuda_stream)), "serq_attn_prefill")
+    if O is None:
+        O = _out_like(Q, stream)
+    ldo = _token_rows(O, "O", cache, T, n_heads)[2]
+    if ws is None:
+        ws = _scratch(_ws_bytes(cache, lib.serq_attn_prefill_ws_bytes, T, n_heads, B, cols, max_kv), cache, stream)
+    else:
+        _check_ws(ws, cache)
+    _call(cache, stream, "serq_attn_prefill", lib.serq_attn_prefill, cache.handle, Q.data_ptr(), ldq, T, n_heads,
+          cache.default_scale if scale is None else scale, B, cu_q.data_ptr(), kv_len.data_ptr(),
+          page_table.data_ptr(), cols, ldt, max_kv, None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel(), O.data_ptr(), ldo)
     return O
 
 
@@ -811,23 +828,19 @@ def attn_decode(cache: KVCache, Q: torch.Tensor, kv_len: torch.Tensor, page_tabl
                 max_kv: int = 0, stream=None) -> torch.Tensor:
     """serq_attn_decode: row b of Q attends to sequence b's kv_len[b] cached
     keys, the first prefix_len of which all sequences share."""
-    n_heads = _token_rows(Q, "Q", cache)
     B, cols, ldt = _batch_args(cache, kv_len, page_table)
-    if Q.shape[0] != B:
-        raise ValueError("Q needs one row per sequence")
-    guard, st = _on(cache, stream)
-    with guard:
-        if O is None:
-            O = _out_like(Q, st)
-        elif _token_rows(O, "O", cache, n_heads) and O.shape[0] != B:
-            raise ValueError("O must have Q's rows")
-        ws = _scratch(lib.serq_attn_decode_ws_bytes(cache.handle, B, n_heads, cols, prefix_len, max_kv)
-                      if ws is None else 0, cache, ws, st)
-        _check(lib.serq_attn_decode(cache.handle, _ptr(Q), _row_stride(Q), n_heads,
-                                    cache.head_dim ** -0.5 if scale is None else scale, B, _ptr(kv_len),
-                                    _ptr(page_table), cols, ldt, prefix_len, max_kv, _ptr(ws),
-                                    0 if ws is None else ws.numel(), _ptr(O), _row_stride(O),
-                                    _vp(st.cuda_stream)), "serq_attn_decode")
+    _, n_heads, ldq = _token_rows(Q, "Q", cache, B)
+    if O is None:
+        O = _out_like(Q, stream)
+    ldo = _token_rows(O, "O", cache, B, n_heads)[2]
+    if ws is None:
+        ws = _scratch(_ws_bytes(cache, lib.serq_attn_decode_ws_bytes, B, n_heads, cols, prefix_len, max_kv), cache,
+                      stream)
+    else:
+        _check_ws(ws, cache)
+    _call(cache, stream, "serq_attn_decode", lib.serq_attn_decode, cache.handle, Q.data_ptr(), ldq, n_heads,
+          cache.default_scale if scale is None else scale, B, kv_len.data_ptr(), page_table.data_ptr(), cols, ldt,
+          prefix_len, max_kv, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), O.data_ptr(), ldo)
     return O
 
 
