@@ -15,8 +15,8 @@
 // TMEM (512 columns): S_A, S_B (128 fp32 columns each; P_X in bf16 takes the
 // first 64 columns of S_X once S_X is in registers), O_A, O_B (D each).
 //
-// Warps: 0-3 softmax of A (one row per thread), 4-7 of B, 8 loads, 9 MMAs
-// (10 and 11 only fill their warpgroup).
+// Warps: 0-3 softmax of A (one row per thread), 4-7 of B, 8 loads, 9 MMAs, 10
+// zeroes values behind the last key (11 only fills the warpgroup).
 // Persistent: a CTA takes work items (tile pair, kv head, key split) and the
 // next item's Q, K and first scores overlap the epilogue of the last one.
 #pragma once
@@ -36,6 +36,7 @@ constexpr int kTileKeys = 128;  // keys of a step
 constexpr int kTcThreads = 384;
 constexpr int kRegsIssue = 88, kRegsSoftmax = 208;
 static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= kTcThreads * 168, "register split");
+constexpr int kFmaPairs = 6;  // of 16 pairs of exponentials, how many go to the FMA pipe
 constexpr float kLazyMax = 8.0f;  // log2: how far a row's scores may exceed the maximum in use
 
 struct TcArgs {
@@ -65,14 +66,16 @@ template <int D>
 struct TcLayout {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = 128 * D * 2;  // bytes of a Q tile, and of a K or V step
-  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr int kSlots = D == 128 ? 5 : 8;
   static constexpr int oQ = 0;
   static constexpr int oKV = 2 * kTile;
   static constexpr int oItem = oKV + kSlots * kTile;
   static constexpr int oBar = oItem + 2 * 64;
-  static constexpr int kBars = 2 * kSlots + 2 * 4 + 4 + 1;
+  static constexpr int kBars = 2 * kSlots + 2 * 8 + 3;
   static constexpr int oMisc = oBar + kBars * 8;
-  static constexpr int kAlloc = oMisc + 16 + 1024;
+  static constexpr int kAlloc = oMisc + 32 + 1024;
+  static_assert(kAlloc <= 232448, "shared memory of a CTA");
+  static_assert(oMisc % 8 == 0, "alignment");
 };
 static_assert(sizeof(Item) <= 64, "item slot");
 
@@ -80,6 +83,31 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 2^y for y <= 8 on the FMA pipe: n = round(y), r = y - n in [-1/2, 1/2], a
+// degree-4 polynomial for 2^r (least maximum relative error with constant term
+// 1, found by reweighted least squares: 2.9e-6, a 1400th of the bf16 rounding that
+// follows), n added to its exponent.  -127 and below give 0.
+__device__ __forceinline__ float2 ex2_fma(float2 y) {
+  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: the sum's low bits are n
+  y.x = fmaxf(y.x, -127.0f);
+  y.y = fmaxf(y.y, -127.0f);
+  const float2 t = add2(y, make_float2(kRound, kRound));
+  const float2 r = add2(y, add2(make_float2(kRound, kRound), make_float2(-t.x, -t.y)));
+  float2 p = make_float2(0.009582852944731712f, 0.009582852944731712f);
+  p = fma2(p, r, make_float2(0.055906426161527634f, 0.055906426161527634f));
+  p = fma2(p, r, make_float2(0.24024099111557007f, 0.24024099111557007f));
+  p = fma2(p, r, make_float2(0.6931241750717163f, 0.6931241750717163f));
+  p = fma2(p, r, make_float2(1.0f, 1.0f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -182,12 +210,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* q_empty = q_full + 2;           // [2] the item's last scores of X are computed
   uint64_t* s_full = q_empty + 2;           // [2] scores ready (and every MMA before them)
   uint64_t* p_full = s_full + 2;            // [2] weights written (and O rescaled)
-  uint64_t* o_full = p_full + 2;            // [2] the item's last product of X is done
+  uint64_t* p_half = p_full + 2;            // [2] the first 64 keys' weights
+  uint64_t* o_full = p_half + 2;            // [2] the item's last product of X is done
   uint64_t* it_full = o_full + 2;           // [2]
   uint64_t* it_empty = it_full + 2;         // [2]
   uint64_t* drain = it_empty + 2;
+  uint64_t* clean_ask = drain + 1;          // values to zero: slot and first row in clean_req
+  uint64_t* clean_done = drain + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::oMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::oMisc + 4);
+  volatile int* clean_req = reinterpret_cast<volatile int*>(smem + L::oMisc + 8);
   auto item_at = [&](int i) -> Item& {
     return *reinterpret_cast<Item*>(reinterpret_cast<uint8_t*>(items) + (i & 1) * 64);
   };
@@ -203,11 +235,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&q_empty[x], 1);
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 4);
+      mbar_init(&p_half[x], 4);
       mbar_init(&o_full[x], 1);
       mbar_init(&it_full[x], 1);
       mbar_init(&it_empty[x], 9);
     }
     mbar_init(drain, 1);
+    mbar_init(clean_ask, 1);
+    mbar_init(clean_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -264,27 +299,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         __syncwarp();
       }
+      // this lane's copy of a step: its page is looked up one step ahead
+      const int half = lane & (L::kHalves - 1), r = lane / L::kHalves * box;
+      auto lookup = [&](int j) {
+        const int key = j * kTileKeys + r;
+        int pg = a.c_.n_pages;  // past the keys that exist: zeros, from outside the map
+        if (lane < copies && key < it.kv_end) {
+          const int e = table[key >> a.c_.page_shift];
+          if (e >= 0 && e < a.c_.n_pages) pg = e;
+          else note_bad_page();
+        }
+        return pg;
+      };
+      int pg_next = it.j0 < end ? lookup(it.j0) : 0;
 #pragma unroll 1
       for (int j = it.j0; j < end && ok; ++j) {
+        const int pg = pg_next;
+        if (j + 1 < end) pg_next = lookup(j + 1);
+        const int y = (it.kvh << a.c_.page_shift) + ((j * kTileKeys + r) & (page - 1));
 #pragma unroll 1
         for (int v = 0; v < 2; ++v) {
           ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[slot], slot_ph ^ 1, abort_flag, kDevTimeoutProducer));
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], L::kTile);
           __syncwarp();
-          if (lane < copies) {
-            const int half = lane & (L::kHalves - 1), r = lane / L::kHalves * box;
-            const int key = j * kTileKeys + r;
-            // past the keys that exist: the copy fills zeros from outside the map
-            int pg = a.c_.n_pages;
-            if (key < it.kv_end) {
-              const int e = table[key >> a.c_.page_shift];
-              if (e >= 0 && e < a.c_.n_pages) pg = e;
-              else note_bad_page();
-            }
+          if (lane < copies)
             tma_load_3d(smem + L::oKV + slot * L::kTile + half * (L::kTile / L::kHalves) + r * 128, v ? &tmV : &tmK,
-                        &kv_full[slot], 64 * half, (it.kvh << a.c_.page_shift) + (key & (page - 1)), pg);
-          }
+                        &kv_full[slot], 64 * half, y, pg);
           __syncwarp();
           if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
         }
@@ -292,110 +333,131 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 9) {
     // ---------------------------------------------------------------- MMAs
-    const uint32_t idesc_qk = umma_idesc_bf16(128, kTileKeys, false, a.neg);
-    constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D, true, false);
-    constexpr int kHalfBytes = L::kTile / L::kHalves;
-    uint32_t slot = 0, slot_ph = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
-    bool ok = true;
-    auto wait = [&](uint64_t* b, uint32_t ph) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(b, ph, abort_flag, kDevTimeoutMma));
-      return ok;
-    };
-    auto scores = [&](int x, uint32_t ks) {
-      const uint64_t dq = umma_desc_k_sw128(smem_u32(smem + L::oQ + x * L::kTile));
-      const uint64_t dk = umma_desc_k_sw128(smem_u32(smem + L::oKV + ks * L::kTile));
+    // One thread runs the whole loop: the tensor core takes a step's 32 MMAs
+    // about as fast as they are issued, so what the issuing thread spends
+    // between them on waits and votes leaves the tensor core idle (with the
+    // whole warp waiting and electing a lane each time, a step of two tiles
+    // took 3400 cycles, 2048 of them MMAs).
+    if (elect_one()) {
+      const uint32_t idesc_qk = umma_idesc_bf16(128, kTileKeys, false, a.neg);
+      constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D, true, false);
+      constexpr int kHalfBytes = L::kTile / L::kHalves;
+      const uint64_t desc_q = umma_desc_k_sw128(smem_u32(smem + L::oQ));
+      const uint64_t desc_k = umma_desc_k_sw128(smem_u32(smem + L::oKV));
+      const uint64_t desc_v = umma_desc_mn_sw128(smem_u32(smem + L::oKV), kHalfBytes);
+      uint32_t slot = 0, slot_ph = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, cn = 0;
+      bool ok = true;
+      auto wait = [&](uint64_t* b, uint32_t ph) { return ok = ok && mbar_wait(b, ph, abort_flag, kDevTimeoutMma); };
+      auto next_slot = [&] {
+        if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
+      };
+      auto scores = [&](int x, uint32_t ks) {
+        const uint64_t dq = desc_q + (uint64_t)(x * (L::kTile >> 4)), dk = desc_k + (uint64_t)(ks * (L::kTile >> 4));
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
-        umma_bf16_ss(tmem + kS + 128u * x, dq + off, dk + off, idesc_qk, k > 0);
-      }
-    };
-    auto values = [&](int x, uint32_t vs, bool acc) {
-      const uint64_t dv = umma_desc_mn_sw128(smem_u32(smem + L::oKV + vs * L::kTile), kHalfBytes);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
+          umma_bf16_ss(tmem + kS + 128u * x, dq + off, dk + off, idesc_qk, k > 0);
+        }
+      };
+      auto values = [&](int x, uint32_t vs, bool acc, int half) {
+        const uint64_t dv = desc_v + (uint64_t)(vs * (L::kTile >> 4));
 #pragma unroll
-      for (int k = 0; k < kTileKeys / 16; ++k)
-        umma_bf16_ts(tmem + kO + (uint32_t)(D * x), tmem + kS + 128u * x + 8u * k, dv + (uint64_t)(128 * k), idesc_pv,
-                     acc || k > 0);
-    };
-    for (int i = 0; ok; ++i) {
-      if (!wait(&it_full[i & 1], (i >> 1) & 1)) break;
-      const Item it = item_at(i);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&it_empty[i & 1]);
-      if (it.done) break;
-      const int end = max(it.endA, it.endB);
-      if (end <= it.j0) continue;
-      auto last = [&](int x) { return x ? it.endB : it.endA; };
-      // scores of the first step
-      if (!wait(&kv_full[slot], slot_ph)) break;
-      for (int x = 0; x < 2; ++x) {
-        if (it.j0 >= last(x)) continue;
-        if (!wait(&q_full[x], qn[x]++ & 1)) break;
-        tc_fence_after();
-        if (elect_one()) {
+        for (int k = half * 4; k < half * 4 + 4; ++k)
+          umma_bf16_ts(tmem + kO + (uint32_t)(D * x), tmem + kS + 128u * x + 8u * k, dv + (uint64_t)(128 * k), idesc_pv,
+                       acc || k > 0);
+      };
+      for (int i = 0; ok; ++i) {
+        if (!wait(&it_full[i & 1], (i >> 1) & 1)) break;
+        const int done = item_at(i).done, j0 = item_at(i).j0, endA = item_at(i).endA, endB = item_at(i).endB;
+        const int kv_end = item_at(i).kv_end;
+        mbar_arrive(&it_empty[i & 1]);
+        if (done) break;
+        const int end = max(endA, endB);
+        if (end <= j0) continue;
+        // scores of the first step
+        if (!wait(&kv_full[slot], slot_ph)) break;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int last = x ? endB : endA;
+          if (j0 >= last || !wait(&q_full[x], qn[x] & 1)) continue;
+          ++qn[x];
+          tc_fence_after();
           scores(x, slot);
           umma_commit<1>(&s_full[x]);
-          if (it.j0 + 1 == last(x)) umma_commit<1>(&q_empty[x]);
+          if (j0 + 1 == last) umma_commit<1>(&q_empty[x]);
         }
-        __syncwarp();
-      }
-      if (!ok) break;
-      if (elect_one()) umma_commit<1>(&kv_empty[slot]);
-      __syncwarp();
-      if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
-      for (int j = it.j0; j < end; ++j) {
-        const uint32_t vs = slot;
-        if (!wait(&kv_full[slot], slot_ph)) break;
-        if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
-        const uint32_t ks = slot;
-        if (j + 1 < end) {
+        if (!ok) break;
+        umma_commit<1>(&kv_empty[slot]);
+        next_slot();
+        for (int j = j0; j < end; ++j) {
+          const uint32_t vs = slot;
           if (!wait(&kv_full[slot], slot_ph)) break;
-          if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
-        }
-        // rows of V behind the last key, up to the end of its page, may hold
-        // anything, and 0 times a NaN is one: zero them
-        const int have = it.kv_end - j * kTileKeys;
-        if (have < kTileKeys) {
-          const int upto = min(kTileKeys, (have + (1 << a.c_.page_shift) - 1) >> a.c_.page_shift << a.c_.page_shift);
-          const int n = (upto - have) * (D / 8);  // 16-byte chunks
-          for (int e = lane; e < n; e += 32) {
-            const int r = have + e / (D / 8), cch = e % (D / 8);
-            *reinterpret_cast<uint4*>(smem + L::oKV + vs * L::kTile + (cch >> 3) * kHalfBytes + r * 128 + (cch & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
+          next_slot();
+          const uint32_t ks = slot;
+          if (j + 1 < end) {
+            if (!wait(&kv_full[slot], slot_ph)) break;
+            next_slot();
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        for (int x = 0; x < 2; ++x) {
-          if (j >= last(x)) continue;
-          if (!wait(&p_full[x], pn[x]++ & 1)) break;
-          tc_fence_after();
-          if (elect_one()) {
-            values(x, vs, j > it.j0);
-            if (j + 1 < last(x)) {
+          if (kv_end - j * kTileKeys < kTileKeys) {  // values that do not exist: see the helper warp
+            clean_req[0] = (int)vs;
+            clean_req[1] = kv_end - j * kTileKeys;
+            mbar_arrive(clean_ask);
+            if (!wait(clean_done, cn++ & 1)) break;
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int last = x ? endB : endA;
+            if (j >= last || !wait(&p_half[x], pn[x] & 1)) continue;
+            tc_fence_after();
+            values(x, vs, j > j0, 0);
+            if (!wait(&p_full[x], pn[x] & 1)) continue;
+            ++pn[x];
+            tc_fence_after();
+            values(x, vs, true, 1);
+            if (j + 1 < last) {
               scores(x, ks);
               umma_commit<1>(&s_full[x]);
-              if (j + 2 == last(x)) umma_commit<1>(&q_empty[x]);
+              if (j + 2 == last) umma_commit<1>(&q_empty[x]);
             } else {
               umma_commit<1>(&o_full[x]);
             }
           }
-          __syncwarp();
-        }
-        if (!ok) break;
-        if (elect_one()) {
+          if (!ok) break;
           umma_commit<1>(&kv_empty[vs]);
           if (j + 1 < end) umma_commit<1>(&kv_empty[ks]);
         }
-        __syncwarp();
       }
-    }
-    // every MMA issued has completed before TMEM and shared memory are freed
-    if (elect_one()) {
+      // every MMA issued has completed before TMEM and shared memory are freed
       umma_commit<1>(drain);
       mbar_wait(drain, 0, nullptr, kDevTimeoutMma);
+      clean_req[0] = -1;
+      mbar_arrive(clean_ask);
     }
     __syncwarp();
+  } else if (warp == 10) {
+    // -------------------------------------------------------------- helper
+    // Rows of V behind the last key, up to the end of its page, may hold
+    // anything, and a zero weight times a NaN is one: on the MMA thread's
+    // request they are zeroed once they have landed.
+    constexpr int kHalfBytes = L::kTile / L::kHalves;
+    for (uint32_t n = 0;; ++n) {
+      // lasts as long as the kernel does: the MMA thread, whose own waits are
+      // bounded, always ends it
+      if (!__all_sync(0xffffffffu, mbar_wait(clean_ask, n & 1, abort_flag, kDevTimeoutMma, 100 * kWaitLimitNs))) break;
+      const int vs = clean_req[0], have = clean_req[1];
+      __syncwarp();
+      if (vs < 0) break;
+      const int upto = min(kTileKeys, (have + (1 << a.c_.page_shift) - 1) >> a.c_.page_shift << a.c_.page_shift);
+      const int chunks = (upto - have) * (D / 8);
+      for (int e = lane; e < chunks; e += 32) {
+        const int r = have + e / (D / 8), c = e % (D / 8);
+        *reinterpret_cast<uint4*>(smem + L::oKV + vs * L::kTile + (c >> 3) * kHalfBytes + r * 128 + (c & 7) * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(clean_done);
+    }
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -426,26 +488,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], sn++ & 1, abort_flag, kDevTimeoutEpilogue));
         if (!ok) break;
         tc_fence_after();
-        uint32_t r[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(tS + 32u * q, r[q]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld_wait_regs(r[q]);
+        // scores in two halves: the maximum of one is taken while the other loads
         const int base = j * kTileKeys;
-        if (base + kTileKeys > warp_lim) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
+        const bool edge = base + kTileKeys > warp_lim;
+        uint32_t r[4][32];
+        float mx[4];
+        auto top = [&](int q) {
+          if (edge) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (base + 32 * q + e >= lim) r[q][e] = 0xff800000u;  // -inf
-        }
-        float mx[4];
+          }
+          float m0 = fmaxf(__uint_as_float(r[q][0]), __uint_as_float(r[q][1]));
+          float m1 = fmaxf(__uint_as_float(r[q][2]), __uint_as_float(r[q][3]));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          mx[q] = __uint_as_float(r[q][0]);
-#pragma unroll
-          for (int e = 1; e < 32; ++e) mx[q] = fmaxf(mx[q], __uint_as_float(r[q][e]));
-        }
+          for (int e = 4; e < 32; e += 4) {
+            m0 = max3(m0, __uint_as_float(r[q][e]), __uint_as_float(r[q][e + 1]));
+            m1 = max3(m1, __uint_as_float(r[q][e + 2]), __uint_as_float(r[q][e + 3]));
+          }
+          mx[q] = fmaxf(m0, m1);
+        };
+        tmem_ld_32x32b_x32(tS, r[0]);
+        tmem_ld_32x32b_x32(tS + 32u, r[1]);
+        tmem_ld_wait_regs(r[0]);
+        tmem_ld_wait_regs(r[1]);
+        tmem_ld_32x32b_x32(tS + 64u, r[2]);
+        tmem_ld_32x32b_x32(tS + 96u, r[3]);
+        top(0);
+        top(1);
+        tmem_ld_wait_regs(r[2]);
+        tmem_ld_wait_regs(r[3]);
+        top(2);
+        top(3);
         const float cand = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
         // the maximum in use follows only when it falls behind by 2^8: weights
         // up to 2^8 cost nothing in bf16 or fp32, and most steps leave O alone
@@ -477,18 +551,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int e = 0; e < 16; ++e) {
             const float2 s2 = make_float2(__uint_as_float(r[q][2 * e]), __uint_as_float(r[q][2 * e + 1]));
             const float2 y = fma2(s2, make_float2(a.c, a.c), make_float2(sub, sub));
-            const float2 p = make_float2(ex2(y.x), ex2(y.y));
+            // the XU pipe's 16 exponentials a cycle would bound the kernel: part
+            // of them is computed on the FMA pipe
+            const float2 p = (e * kFmaPairs) % 16 < kFmaPairs ? ex2_fma(y) : make_float2(ex2(y.x), ex2(y.y));
             if (e & 1) sum1 = add2(sum1, p);
             else sum0 = add2(sum0, p);
             const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
             w[e] = reinterpret_cast<const uint32_t&>(h);
           }
           tmem_st_32x32b_x16(tS + 16u * q, w);
+          if (q & 1) {  // half of the keys: their product may start
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q == 1 ? &p_half[x] : &p_full[x]);
+          }
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
         l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
       }
       if (!ok) break;
