@@ -16,12 +16,13 @@
 // first 64 columns of S_X once S_X is in registers), O_A, O_B (D each).
 //
 // Warps: 0-3 softmax of A (one row per thread), 4-7 of B, 8 loads, 9 MMAs, 10
-// zeroes values behind the last key (11 only fills the warpgroup).
+// zeroes values behind the last key, 11 decodes work items ahead.
 // Persistent: a CTA takes work items (tile pair, kv head, key split) and the
 // next item's Q, K and first scores overlap the epilogue of the last one.
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "rope.cuh"
 
@@ -66,10 +67,11 @@ template <int D>
 struct TcLayout {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = 128 * D * 2;  // bytes of a Q tile, and of a K or V step
-  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kSlots = D == 128 ? 4 : 8;
   static constexpr int oQ = 0;
   static constexpr int oKV = 2 * kTile;
-  static constexpr int oItem = oKV + kSlots * kTile;
+  static constexpr int oStage = oKV + kSlots * kTile;  // 4 KB per softmax warp
+  static constexpr int oItem = oStage + 8 * 4096;
   static constexpr int oBar = oItem + 2 * 64;
   static constexpr int kBars = 2 * kSlots + 2 * 8 + 3;
   static constexpr int oMisc = oBar + kBars * 8;
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&p_half[x], 4);
       mbar_init(&o_full[x], 1);
       mbar_init(&it_full[x], 1);
-      mbar_init(&it_empty[x], 9);
+      mbar_init(&it_empty[x], 10);
     }
     mbar_init(drain, 1);
     mbar_init(clean_ask, 1);
@@ -264,24 +266,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
     }
-    grid_dep_wait();
-    grid_dep_launch();
     const int page = 1 << a.c_.page_shift;
     const int box = min(page, kTileKeys);         // rows per copy
     const int copies = kTileKeys / box * L::kHalves;  // per step and operand
     uint32_t slot = 0, slot_ph = 0, qn[2] = {0, 0};
     bool ok = true;
     for (int i = 0; ok; ++i) {
-      Item it;
-      // every other round backwards: the items come in falling cost, so that
-      // each CTA's sum stays near the mean
-      decode_item(a, i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, it);
-      ok = __all_sync(0xffffffffu, mbar_wait(&it_empty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag, kDevTimeoutProducer));
-      if (!ok) break;
-      if (lane == 0) {
-        item_at(i) = it;
-        mbar_arrive(&it_full[i & 1]);
-      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&it_full[i & 1], (i >> 1) & 1, abort_flag, kDevTimeoutProducer))) break;
+      const Item it = item_at(i);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&it_empty[i & 1]);
       if (it.done) break;
       const int32_t* table = a.b.table + (long long)it.seq * a.b.ldt;
       const int end = max(it.endA, it.endB);
@@ -319,7 +313,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int y = (it.kvh << a.c_.page_shift) + ((j * kTileKeys + r) & (page - 1));
 #pragma unroll 1
         for (int v = 0; v < 2; ++v) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[slot], slot_ph ^ 1, abort_flag, kDevTimeoutProducer));
+          ok = __all_sync(0xffffffffu, mbar_wait_idle(&kv_empty[slot], slot_ph ^ 1, abort_flag, kDevTimeoutProducer, kWaitLimitNs));
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], L::kTile);
           __syncwarp();
@@ -443,7 +437,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (uint32_t n = 0;; ++n) {
       // lasts as long as the kernel does: the MMA thread, whose own waits are
       // bounded, always ends it
-      if (!__all_sync(0xffffffffu, mbar_wait(clean_ask, n & 1, abort_flag, kDevTimeoutMma, 100 * kWaitLimitNs))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait_idle(clean_ask, n & 1, abort_flag, kDevTimeoutMma, 100 * kWaitLimitNs))) break;
       const int vs = clean_req[0], have = clean_req[1];
       __syncwarp();
       if (vs < 0) break;
@@ -457,6 +451,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(clean_done);
+    }
+  } else {
+    // ----------------------------------------------------------- scheduling
+    // Decodes the CTA's work items ahead of their use.
+    grid_dep_wait();
+    grid_dep_launch();
+    for (int i = 0;; ++i) {
+      Item it;
+      // every other round backwards: the items come in falling cost, so that
+      // each CTA's sum stays near the mean
+      decode_item(a, i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, it);
+      if (!__all_sync(0xffffffffu, mbar_wait_idle(&it_empty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag,
+                                                  kDevTimeoutProducer, 100 * kWaitLimitNs)))
+        break;
+      if (lane == 0) {
+        item_at(i) = it;
+        mbar_arrive(&it_full[i & 1]);
+      }
+      if (it.done) break;
     }
   }
   } else {
@@ -488,86 +501,104 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], sn++ & 1, abort_flag, kDevTimeoutEpilogue));
         if (!ok) break;
         tc_fence_after();
-        // scores in two halves: the maximum of one is taken while the other loads
+        // The scores are read from TMEM twice, for the maximum and for the
+        // weights: held in registers in between, they left too few for the
+        // exponentials' temporaries (spills; 750 cycles per 64 keys, not 560).
         const int base = j * kTileKeys;
-        const bool edge = base + kTileKeys > warp_lim;
-        uint32_t r[4][32];
-        float mx[4];
-        auto top = [&](int q) {
-          if (edge) {
+        auto step = [&](auto edge_tag) {
+          constexpr bool kEdge = decltype(edge_tag)::value;
+          auto mask = [&](uint32_t(&r)[32], int q) {
+            if (kEdge && base + 32 * q + 32 > warp_lim) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (base + 32 * q + e >= lim) r[q][e] = 0xff800000u;  // -inf
-          }
-          float m0 = fmaxf(__uint_as_float(r[q][0]), __uint_as_float(r[q][1]));
-          float m1 = fmaxf(__uint_as_float(r[q][2]), __uint_as_float(r[q][3]));
+              for (int e = 0; e < 32; ++e)
+                if (base + 32 * q + e >= lim) r[e] = 0xff800000u;  // -inf
+            }
+          };
+          float mx[2];
+          {
+            uint32_t r[4][32];
+            tmem_ld_32x32b_x32(tS, r[0]);
+            tmem_ld_32x32b_x32(tS + 32u, r[1]);
+            tmem_ld_wait_regs(r[0]);
+            tmem_ld_wait_regs(r[1]);
+            tmem_ld_32x32b_x32(tS + 64u, r[2]);
+            tmem_ld_32x32b_x32(tS + 96u, r[3]);
 #pragma unroll
-          for (int e = 4; e < 32; e += 4) {
-            m0 = max3(m0, __uint_as_float(r[q][e]), __uint_as_float(r[q][e + 1]));
-            m1 = max3(m1, __uint_as_float(r[q][e + 2]), __uint_as_float(r[q][e + 3]));
-          }
-          mx[q] = fmaxf(m0, m1);
-        };
-        tmem_ld_32x32b_x32(tS, r[0]);
-        tmem_ld_32x32b_x32(tS + 32u, r[1]);
-        tmem_ld_wait_regs(r[0]);
-        tmem_ld_wait_regs(r[1]);
-        tmem_ld_32x32b_x32(tS + 64u, r[2]);
-        tmem_ld_32x32b_x32(tS + 96u, r[3]);
-        top(0);
-        top(1);
-        tmem_ld_wait_regs(r[2]);
-        tmem_ld_wait_regs(r[3]);
-        top(2);
-        top(3);
-        const float cand = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
-        // the maximum in use follows only when it falls behind by 2^8: weights
-        // up to 2^8 cost nothing in bf16 or fp32, and most steps leave O alone
-        const bool grow = valid && cand > mc + kLazyMax;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float f = grow ? ex2(mc - cand) : 1.0f;
-          if (grow) {
-            mc = cand;
-            l *= f;
-          }
-          if (j > it.j0) {
-#pragma unroll 1
-            for (int q = 0; q < D / 16; ++q) {
-              uint32_t o[16];
-              tmem_ld_32x32b_x16(tO + 16u * q, o);
-              tmem_ld_wait_regs(o);
+            for (int q = 0; q < 4; ++q) {
+              if (q == 2) {
+                tmem_ld_wait_regs(r[2]);
+                tmem_ld_wait_regs(r[3]);
+              }
+              mask(r[q], q);
+              if (q == 0) {
+                mx[0] = __uint_as_float(r[0][0]);
+                mx[1] = __uint_as_float(r[0][1]);
+              }
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st_32x32b_x16(tO + 16u * q, o);
+              for (int e = q ? 0 : 2; e < 30; e += 4) {
+                mx[0] = max3(mx[0], __uint_as_float(r[q][e]), __uint_as_float(r[q][e + 1]));
+                mx[1] = max3(mx[1], __uint_as_float(r[q][e + 2]), __uint_as_float(r[q][e + 3]));
+              }
+              if (q == 0) mx[0] = max3(mx[0], __uint_as_float(r[0][30]), __uint_as_float(r[0][31]));
             }
           }
-        }
-        const float sub = mc == -INFINITY ? 0.f : -mc;
-        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+          uint32_t s[2][32];
+          tmem_ld_32x32b_x32(tS, s[0]);
+          const float cand = fmaxf(mx[0], mx[1]) * a.c;
+          // the maximum in use follows only when it falls behind by 2^8: weights
+          // up to 2^8 cost nothing in bf16 or fp32, and most steps leave O alone
+          const bool grow = valid && cand > mc + kLazyMax;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float f = grow ? ex2(mc - cand) : 1.0f;
+            if (grow) {
+              mc = cand;
+              l *= f;
+            }
+            if (j > it.j0) {
+#pragma unroll 1
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(tO + 16u * q, o);
+                tmem_ld_wait_regs(o);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t w[16];
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st_32x32b_x16(tO + 16u * q, o);
+              }
+            }
+          }
+          const float sub = mc == -INFINITY ? 0.f : -mc;
+          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 s2 = make_float2(__uint_as_float(r[q][2 * e]), __uint_as_float(r[q][2 * e + 1]));
-            const float2 y = fma2(s2, make_float2(a.c, a.c), make_float2(sub, sub));
-            // the XU pipe's 16 exponentials a cycle would bound the kernel: part
-            // of them is computed on the FMA pipe
-            const float2 p = (e * kFmaPairs) % 16 < kFmaPairs ? ex2_fma(y) : make_float2(ex2(y.x), ex2(y.y));
-            if (e & 1) sum1 = add2(sum1, p);
-            else sum0 = add2(sum0, p);
-            const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
-            w[e] = reinterpret_cast<const uint32_t&>(h);
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld_wait_regs(s[q & 1]);
+            if (q < 3) tmem_ld_32x32b_x32(tS + 32u * (q + 1), s[(q + 1) & 1]);
+            mask(s[q & 1], q);
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 s2 = make_float2(__uint_as_float(s[q & 1][2 * e]), __uint_as_float(s[q & 1][2 * e + 1]));
+              const float2 y = fma2(s2, make_float2(a.c, a.c), make_float2(sub, sub));
+              // the XU pipe's 16 exponentials a cycle would bound the kernel: part
+              // of them is computed on the FMA pipe
+              const float2 p = (e * kFmaPairs) % 16 < kFmaPairs ? ex2_fma(y) : make_float2(ex2(y.x), ex2(y.y));
+              if (e & 1) sum1 = add2(sum1, p);
+              else sum0 = add2(sum0, p);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
+              w[e] = reinterpret_cast<const uint32_t&>(h);
+            }
+            // columns 16 q ... of weights lie on scores that have been read
+            tmem_st_32x32b_x16(tS + 16u * q, w);
+            if (q & 1) {  // half of the keys: their product may start
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(q == 1 ? &p_half[x] : &p_full[x]);
+            }
           }
-          tmem_st_32x32b_x16(tS + 16u * q, w);
-          if (q & 1) {  // half of the keys: their product may start
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q == 1 ? &p_half[x] : &p_full[x]);
-          }
-        }
-        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+          l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+        };
+        if (base + kTileKeys > warp_lim) step(std::true_type{});
+        else step(std::false_type{});
       }
       if (!ok) break;
       // -------------------------------------------------------- epilogue
@@ -598,28 +629,42 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       } else {
-        __nv_bfloat16* dst = a.o + (long long)t * a.ldo + (long long)h * D;
+        // 64 columns at a time through the warp's 4 KB of shared memory, so that
+        // rows leave as whole 128-byte lines (16-byte chunks swizzled by the row)
+        __nv_bfloat16* dst = valid ? a.o + (long long)t * a.ldo + (long long)h * D : nullptr;
+        uint8_t* stage = smem + L::oStage + warp * 4096;
 #pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
+        for (int q = 0; q < D / 64; ++q) {
+          uint32_t o[2][32];
           if (any) {
-            tmem_ld_32x32b_x32(tO + 32u * q, o);
-            tmem_ld_wait_regs(o);
+            tmem_ld_32x32b_x32(tO + 64u * q, o[0]);
+            tmem_ld_32x32b_x32(tO + 64u * q + 32u, o[1]);
+            tmem_ld_wait_regs(o[0]);
+            tmem_ld_wait_regs(o[1]);
           }
-          if (valid) {
-            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < 8; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
               // a row that saw no key has inv = 0 and is written as zeros
-              const float v0 = l > 0.f ? __uint_as_float(o[2 * e]) * inv : 0.f;
-              const float v1 = l > 0.f ? __uint_as_float(o[2 * e + 1]) * inv : 0.f;
+              const float v0 = l > 0.f ? __uint_as_float(o[e >> 2][(8 * e + 2 * k) & 31]) * inv : 0.f;
+              const float v1 = l > 0.f ? __uint_as_float(o[e >> 2][(8 * e + 2 * k + 1) & 31]) * inv : 0.f;
               const __nv_bfloat162 b2 = __floats2bfloat162_rn(v0, v1);
-              w[e] = reinterpret_cast<const uint32_t&>(b2);
+              w[k] = reinterpret_cast<const uint32_t&>(b2);
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              reinterpret_cast<uint4*>(dst + 32 * q)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int rr = 4 * e + (lane >> 3), ch = lane & 7;
+            __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), rr));
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
+            if (to != nullptr) *reinterpret_cast<uint4*>(to + 64 * q + 8 * ch) = v;
+          }
+          __syncwarp();
         }
       }
       // the next item's first product overwrites O: its weights are only
