@@ -37,9 +37,9 @@ struct DecArgs {
   int shares;   // G
   float* so;    // slots [2 G (+ batch x blocks of heads when prefix)][rows][D], normalised
   float* slse;  // [slot][rows]
-  const float* po;    // prefix partials [split][batch][n_heads][D]
+  const float* po;    // the prefix pass's slots [slot][256][D] and their log-sums
   const float* plse;
-  int psplits;
+  int ptokens, pshares;  // its tokens per tile and shares
   BatchArgs b;
   CacheArgs c_;
 };
@@ -475,16 +475,40 @@ __global__ void __launch_bounds__(128) k_join(const DecArgs a) {
     c0 = (int)(((s0 + 1) * a.shares - 1) / total);  // largest c with floor(total c / shares) <= s0
     c1 = (int)((s1 * a.shares - 1) / total);
   }
+  // the prefix's parts, as ShareWalk lays them out: pairs of `keys` keys each
+  int p0 = 0, np = 0, item = 0, prow = 0;
+  long long pstart = 0, ptotal = 1, keys = 0;
+  if (a.prefix) {
+    int k = 0;
+    for (int i = lane; i < a.b.batch; i += 32) k = max(k, min(a.b.kv_len[i], a.prefix));
+    keys = __reduce_max_sync(0xffffffffu, k);
+    if (keys > 0) {
+      const int pair = 2 * a.ptokens, pairs = ceil_div(a.b.batch, pair), tile = b / pair;
+      const int in = b - tile * pair, x = in >= a.ptokens;
+      prow = 128 * x + (in - x * a.ptokens) * a.group + hr;
+      item = kvh * pairs + tile;
+      pstart = item * keys;
+      ptotal = keys * pairs * a.c_.n_kv_heads;
+      p0 = (int)(((pstart + 1) * a.pshares - 1) / ptotal);
+      np = (int)(((pstart + keys) * a.pshares - 1) / ptotal) - p0 + 1;
+    }
+  }
   grid_dep_wait();
   if (nb > 0 && c0 == c1 && a.prefix == 0) return;  // finished by its CTA
-  const int np = a.prefix ? a.psplits : 0, n = np + c1 - c0 + 1;
+  const int n = np + c1 - c0 + 1;
   // part i: log-sum and place of its row (in rows of D floats)
   auto find = [&](int i, const float*& src) {
     float lse = -INFINITY;
     if (i < np) {
-      const long long at = ((long long)i * a.b.batch + b) * a.n_heads + h;
-      lse = a.plse[at];
-      src = a.po + at * D;
+      const long long c = p0 + i;
+      const long long lo = max(0ll, ptotal * c / a.pshares - pstart), hi = min(keys, ptotal * (c + 1) / a.pshares - pstart);
+      const int steps = ceil_div((int)keys, kTileKeys);
+      const int shi = hi == keys ? steps : (int)(hi / kTileKeys);
+      if (lo < hi && lo / kTileKeys < shi) {  // else: no step of its own
+        const long long slot = lo > 0 ? 2 * c : hi < keys ? 2 * c + 1 : 2ll * a.pshares + item;
+        lse = a.plse[slot * 256 + prow];
+        src = a.po + (slot * 256 + prow) * D;
+      }
     } else if (i < n) {
       const long long c = c0 + i - np, w0 = total * c / a.shares, w1 = total * (c + 1) / a.shares;
       if (w0 < w1) {  // else: fewer blocks than shares

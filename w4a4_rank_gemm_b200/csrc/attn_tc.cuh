@@ -41,14 +41,14 @@ constexpr int kFmaPairs = 6;  // of 16 pairs of exponentials, how many go to the
 constexpr float kLazyMax = 8.0f;  // log2: how far a row's scores may exceed the maximum in use
 
 struct TcArgs {
-  __nv_bfloat16* o;  // po == nullptr
+  __nv_bfloat16* o;
   long long ldo;
-  float* po;         // partial outputs [split][token][head][D], normalised
-  float* plse;       // and log2 of their sums [split][token][head], -inf: nothing
+  float* po;    // partial outputs [slot][row of the pair][D], normalised
+  float* plse;  // and log2 of their sums [slot][row of the pair], -inf: nothing
   float c;           // |scale| log2 e, never 0
   int neg;           // scale < 0: the product is taken with -Q
   int T, n_heads, group, tokens;  // tokens: per tile, 128 / group
-  int splits;
+  int shares;        // > 0: equal shares of the work for that many CTAs; 0: whole items
   int prefix;        // > 0: decode rows; every row is at sequence 0's first `prefix` keys, up to its own kv_len
   BatchArgs b;
   CacheArgs c_;
@@ -60,7 +60,8 @@ struct Item {
   int row0, n_tok;     // first token row, tokens of the pair
   int lim0;            // keys that the first token sees (causal: one more for each next)
   int kv_end;          // keys that exist
-  int kvh, split, seq;
+  int kvh, seq;
+  int slot;            // of the partial output; -1: the item's rows are finished here
 };
 
 template <int D>
@@ -114,87 +115,272 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Decodes work item w (the whole warp calls): items run over (tile pair, last
-// first), kv head, key split.
-__device__ __forceinline__ void decode_item(const TcArgs& a, int w, int lane, Item& it) {
+// A sequence's tile pairs: pair i holds tokens [i pair, (i + 1) pair) and sees
+// the keys up to its last token.
+struct Pairs {
+  int n, first, kv;  // query rows, first row, cached tokens
+  int np;            // tile pairs
+  int keys;          // of kv, those that the page table holds
+};
+
+__device__ __forceinline__ Pairs load_pairs(const TcArgs& a, int b) {
   const int pair = 2 * a.tokens;
-  it.split = w % a.splits;
-  w /= a.splits;
-  it.kvh = w % a.c_.n_kv_heads;
-  w /= a.c_.n_kv_heads;
-  const int cap = a.b.max_pages << a.c_.page_shift;
-  it.done = 0;
-  int seq = 0, tile = w, first = 0, n = 0, kv = 0;
-  if (a.prefix) {
-    n = a.T;
-    const int tiles = ceil_div(n, pair);
-    if (w >= tiles) it.done = 1;
-  } else {
-    // the w-th tile pair from the back
-    int total = 0, kv_mine = 0;
-    for (int b0 = 0; b0 < a.b.batch; b0 += 32) {
-      const int b = b0 + lane;
-      const int nb = b < a.b.batch ? max(0, a.b.cu_q[b + 1] - a.b.cu_q[b]) : 0;
-      kv_mine = b < a.b.batch ? a.b.kv_len[b] : 0;  // read with the offsets, not after them
-      total += __reduce_add_sync(0xffffffffu, ceil_div(nb, pair));
-    }
-    if (w >= total) {
-      it.done = 1;
-    } else {
-      int left = total - 1 - w;
-      for (int b0 = 0; b0 < a.b.batch; b0 += 32) {
-        const int b = b0 + lane;
-        const int nb = b < a.b.batch ? max(0, a.b.cu_q[b + 1] - a.b.cu_q[b]) : 0;
-        const int from = b < a.b.batch ? a.b.cu_q[b] : 0;
-        if (a.b.batch > 32) kv_mine = b < a.b.batch ? a.b.kv_len[b] : 0;
-        const int mine = ceil_div(nb, pair);
-        int incl = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, incl, d);
-          if (lane >= d) incl += v;
-        }
-        const int sum = __shfl_sync(0xffffffffu, incl, 31);
-        if (left < sum) {
-          const uint32_t hit = __ballot_sync(0xffffffffu, left < incl);
-          const int src = __ffs(hit) - 1;
-          seq = b0 + src;
-          tile = left - (__shfl_sync(0xffffffffu, incl, src) - __shfl_sync(0xffffffffu, mine, src));
-          n = __shfl_sync(0xffffffffu, nb, src);
-          first = __shfl_sync(0xffffffffu, from, src);
-          kv = __shfl_sync(0xffffffffu, kv_mine, src);
-          break;
-        }
-        left -= sum;
-      }
-    }
+  Pairs s = {0, 0, 0, 0, 0};
+  if (a.prefix == 0 && b < a.b.batch) {
+    s.first = a.b.cu_q[b];
+    s.n = max(0, a.b.cu_q[b + 1] - s.first);
+    s.kv = a.b.kv_len[b];
+    s.np = ceil_div(s.n, pair);
+    s.keys = max(0, min(s.kv, a.b.max_pages << a.c_.page_shift));
   }
-  if (it.done) return;
-  it.row0 = first + tile * pair;
-  it.n_tok = min(pair, n - tile * pair);
+  return s;
+}
+
+// Keys and steps of pair i.
+__device__ __forceinline__ int pair_steps(const Pairs& s, int i, int pair) {
+  return ceil_div(max(0, min(s.keys, s.kv - s.n + min(s.n, (i + 1) * pair))), kTileKeys);
+}
+
+// The item of pair `tile` of sequence `seq` and kv head, steps [lo, hi).
+__device__ __forceinline__ void fill_item(const TcArgs& a, const Pairs& s, int seq, int tile, int kvh, int lo, int hi,
+                                          Item& it) {
+  const int pair = 2 * a.tokens;
+  it.done = 0;
+  it.seq = seq;
+  it.kvh = kvh;
+  it.row0 = s.first + tile * pair;
+  it.n_tok = min(pair, s.n - tile * pair);
+  it.kv_end = s.keys;
   int limA, limB;  // most keys that a row of the tile sees
   if (a.prefix) {
-    int m = 0;
-    for (int b = lane; b < a.b.batch; b += 32) m = max(m, min(a.b.kv_len[b], a.prefix));
-    it.kv_end = __reduce_max_sync(0xffffffffu, m);
     it.lim0 = 0;
-    limA = limB = it.kv_end;
+    limA = limB = s.keys;
   } else {
-    it.kv_end = max(0, min(kv, cap));
-    if (kv > cap && lane == 0) note_bad_page();
-    it.lim0 = kv - n + tile * pair + 1;
-    limA = min(it.kv_end, it.lim0 + min(a.tokens, it.n_tok) - 1);
-    limB = min(it.kv_end, it.lim0 + it.n_tok - 1);
+    it.lim0 = s.kv - s.n + tile * pair + 1;
+    limA = min(s.keys, it.lim0 + min(a.tokens, it.n_tok) - 1);
+    limB = min(s.keys, it.lim0 + it.n_tok - 1);
+    if (s.kv > s.keys && s.kv > 0) note_bad_page();
   }
-  const int nA = ceil_div(max(limA, 0), kTileKeys);
-  const int nB = it.n_tok > a.tokens ? ceil_div(max(limB, 0), kTileKeys) : 0;
-  const int steps = max(nA, nB);
-  const int per = ceil_div(steps, a.splits);
-  it.j0 = it.split * per;
-  it.endA = min(nA, it.j0 + per);
-  it.endB = min(nB, it.j0 + per);
-  it.seq = seq;
+  it.j0 = lo;
+  it.endA = min(hi, ceil_div(max(limA, 0), kTileKeys));
+  it.endB = it.n_tok > a.tokens ? min(hi, ceil_div(max(limB, 0), kTileKeys)) : 0;
 }
+
+// Whole items in falling cost.  `mine` is lane's sequence (batch <= 32), so
+// that an item is found without touching memory: the r-th costliest pair has
+// the largest number of steps X with more than r pairs of at least X, counted
+// per sequence in closed form.  Batches above 32 take pairs from the back.
+__device__ __forceinline__ void ranked_item(const TcArgs& a, const Pairs& mine, int w, int lane, Item& it) {
+  const int pair = 2 * a.tokens, heads = a.c_.n_kv_heads;
+  const int r = w / heads, kvh = w - r * heads;
+  it.slot = -1;
+  it.done = 1;
+  if (a.b.batch <= 32) {
+    const int total = __reduce_add_sync(0xffffffffu, mine.np);
+    if (r >= total) return;
+    auto at_least = [&](int x) {  // this lane's pairs of at least x steps
+      if (x <= 0) return mine.np;
+      const int v = (x - 1) * kTileKeys;
+      if (mine.np == 0 || min(mine.keys, mine.kv) <= v) return 0;
+      return mine.np - min(mine.np, max(0, v - (mine.kv - mine.n)) / pair);
+    };
+    int x = 0;
+    if (total * heads > (int)gridDim.x) {
+      int hi = __reduce_max_sync(0xffffffffu, ceil_div(mine.keys, kTileKeys)) + 1;
+      while (hi - x > 1) {
+        const int mid = (x + hi) >> 1;
+        if ((int)__reduce_add_sync(0xffffffffu, at_least(mid)) > r) x = mid;
+        else hi = mid;
+      }
+    } else {
+      x = -1;  // one round: any order
+    }
+    const int ge = x < 0 ? mine.np : at_least(x), gt = x < 0 ? 0 : at_least(x + 1);
+    const int left = r - (int)__reduce_add_sync(0xffffffffu, gt), eq = ge - gt;
+    int incl = eq;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, left < incl)) - 1;
+    const int tile = __shfl_sync(0xffffffffu, mine.np - ge + left - (incl - eq), src);
+    Pairs s;
+    s.n = __shfl_sync(0xffffffffu, mine.n, src);
+    s.first = __shfl_sync(0xffffffffu, mine.first, src);
+    s.kv = __shfl_sync(0xffffffffu, mine.kv, src);
+    s.np = 0;
+    s.keys = __shfl_sync(0xffffffffu, mine.keys, src);
+    fill_item(a, s, src, tile, kvh, 0, 0x7fffffff, it);
+    return;
+  }
+  int total = 0;
+  for (int b0 = 0; b0 < a.b.batch; b0 += 32)
+    total += __reduce_add_sync(0xffffffffu, load_pairs(a, b0 + lane).np);
+  if (r >= total) return;
+  int left = total - 1 - r;
+  for (int b0 = 0;; b0 += 32) {
+    const Pairs p = load_pairs(a, b0 + lane);
+    int incl = p.np;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, left < incl);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const int tile = __shfl_sync(0xffffffffu, left - (incl - p.np), src);
+      fill_item(a, load_pairs(a, b0 + src), b0 + src, tile, kvh, 0, 0x7fffffff, it);
+      return;
+    }
+    left -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+// Equal shares.  Work is laid out by sequence, kv head and tile pair and
+// measured in keys, m_i = past + (i + 1) pair for pair i (every pair of the
+// shared prefix: its keys), whose sums have a closed form; share c of G is
+// [W c / G, W (c + 1) / G).  An item cut at key x is cut at step x / 128.
+struct Measure {
+  long long past, inc;  // m_i = past + (i + 1) inc
+  __device__ long long of(int i) const { return past + (i + 1) * inc; }
+  __device__ long long before(long long i) const { return i * past + inc * (i * (i + 1) / 2); }
+};
+__device__ __forceinline__ Measure measure(const TcArgs& a, const Pairs& s) {
+  Measure m;
+  m.past = a.prefix ? s.keys : max(0, s.kv - s.n);
+  m.inc = a.prefix ? 0 : 2 * a.tokens;
+  return m;
+}
+
+// The one pseudo-sequence of a decode batch's shared prefix (the warp calls).
+__device__ __forceinline__ Pairs prefix_pairs(const TcArgs& a, int lane) {
+  int m = 0;
+  for (int b = lane; b < a.b.batch; b += 32) m = max(m, min(a.b.kv_len[b], a.prefix));
+  Pairs s;
+  s.n = a.T;
+  s.first = 0;
+  s.kv = s.keys = __reduce_max_sync(0xffffffffu, m);
+  s.np = s.keys ? ceil_div(a.T, 2 * a.tokens) : 0;
+  return s;
+}
+
+// Work of one kv head over the sequences before b, and over all (the warp calls).
+__device__ __forceinline__ void share_sums(const TcArgs& a, int b, int lane, long long& before, long long& total) {
+  long long lo = 0, all = 0;
+  for (int i = lane; i < a.b.batch; i += 32) {
+    const Pairs s = load_pairs(a, i);
+    const long long m = measure(a, s).before(s.np);
+    all += m;
+    if (i < b) lo += m;
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    lo += __shfl_xor_sync(0xffffffffu, lo, d);
+    all += __shfl_xor_sync(0xffffffffu, all, d);
+  }
+  before = lo;
+  total = all;
+}
+
+// The next segment of a share; state is the same in every lane.
+struct ShareWalk {
+  long long x, x1;  // position, end
+  long long start;  // of the current item
+  int seq, kvh, tile;
+  Pairs s;
+
+  // `one`: the lane's sequence when the batch fits a warp (or the prefix's).
+  __device__ void init(const TcArgs& a, int lane) {
+    const int heads = a.c_.n_kv_heads;
+    long long before = 0, total;
+    if (a.prefix) {
+      s = prefix_pairs(a, lane);
+      total = measure(a, s).before(s.np);
+    } else {
+      share_sums(a, 0, lane, before, total);
+    }
+    total *= heads;
+    x = total * blockIdx.x / a.shares;
+    x1 = total * (blockIdx.x + 1) / a.shares;
+    if (x >= x1) return;
+    seq = 0;
+    long long base = 0, per_head = 0;
+    if (a.prefix) {
+      per_head = total / heads;
+    } else {
+      for (int b0 = 0;; b0 += 32) {
+        const Pairs p = load_pairs(a, b0 + lane);
+        const long long m = measure(a, p).before(p.np);
+        long long incl = m;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += v;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, x < (base + incl) * heads);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          seq = b0 + src;
+          per_head = __shfl_sync(0xffffffffu, m, src);
+          base += __shfl_sync(0xffffffffu, incl, src) - per_head;
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      s = load_pairs(a, seq);
+    }
+    const long long rest = x - base * heads;
+    kvh = (int)(rest / per_head);
+    const long long in = rest - kvh * per_head;
+    const Measure m = measure(a, s);
+    int lo = 0, hi = s.np;  // the tile with before(lo) <= in < before(lo + 1)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (m.before(mid) <= in) lo = mid;
+      else hi = mid;
+    }
+    tile = lo;
+    start = base * heads + kvh * per_head + m.before(lo);
+  }
+
+  // False: the share is finished.  Segments without a step are passed over.
+  __device__ bool next(const TcArgs& a, Item& it) {
+    const int heads = a.c_.n_kv_heads;
+    while (x < x1) {
+      const long long size = measure(a, s).of(tile);
+      const int steps = a.prefix ? ceil_div(s.keys, kTileKeys) : pair_steps(s, tile, 2 * a.tokens);
+      const long long lo = x - start, hi = min(x1 - start, size);
+      const int slo = (int)min((long long)steps, lo / kTileKeys);
+      const int shi = hi == size ? steps : (int)min((long long)steps, hi / kTileKeys);
+      const bool emit = shi > slo || (steps == 0 && lo == 0);
+      if (emit) {
+        fill_item(a, s, seq, tile, kvh, slo, shi, it);
+        it.slot = a.prefix == 0 && slo == 0 && shi == steps ? -1
+                  : lo > 0                                  ? 2 * blockIdx.x
+                  : hi < size                               ? 2 * blockIdx.x + 1
+                                                            : 2 * a.shares + kvh * s.np + tile;
+      }
+      x = start + hi;
+      if (hi == size) {
+        start += size;
+        if (++tile == s.np) {
+          tile = 0;
+          if (++kvh == heads) {
+            kvh = 0;
+            if (x < x1) {  // then another sequence with rows follows
+              do s = load_pairs(a, ++seq);
+              while (s.np == 0);
+            }
+          }
+        }
+      }
+      if (emit) return true;
+    }
+    return false;
+  }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -279,20 +465,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (it.done) break;
       const int32_t* table = a.b.table + (long long)it.seq * a.b.ldt;
       const int end = max(it.endA, it.endB);
-#pragma unroll 1
-      for (int x = 0; x < 2 && ok; ++x) {
-        if ((x ? it.endB : it.endA) <= it.j0) continue;
-        ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[x], (qn[x] & 1) ^ 1, abort_flag, kDevTimeoutProducer));
-        if (!ok) break;
-        ++qn[x];
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full[x], a.tokens * a.group * D * 2);
-          for (int h = 0; h < L::kHalves; ++h)
-            tma_load_3d(smem + L::oQ + x * L::kTile + h * (L::kTile / L::kHalves), &tmQ, &q_full[x], 64 * h,
-                        it.kvh * a.group, it.row0 + x * a.tokens);
-        }
-        __syncwarp();
-      }
       // this lane's copy of a step: its page is looked up one step ahead
       const int half = lane & (L::kHalves - 1), r = lane / L::kHalves * box;
       auto lookup = [&](int j) {
@@ -305,24 +477,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         return pg;
       };
-      int pg_next = it.j0 < end ? lookup(it.j0) : 0;
+      auto load = [&](const CUtensorMap* tm, int j, int pg) {
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_idle(&kv_empty[slot], slot_ph ^ 1, abort_flag, kDevTimeoutProducer, kWaitLimitNs));
+        if (!ok) return;
+        if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], L::kTile);
+        __syncwarp();
+        if (lane < copies)
+          tma_load_3d(smem + L::oKV + slot * L::kTile + half * (L::kTile / L::kHalves) + r * 128, tm, &kv_full[slot],
+                      64 * half, (it.kvh << a.c_.page_shift) + ((j * kTileKeys + r) & (page - 1)), pg);
+        __syncwarp();
+        if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
+      };
+      int pg = it.j0 < end ? lookup(it.j0) : 0;
 #pragma unroll 1
       for (int j = it.j0; j < end && ok; ++j) {
-        const int pg = pg_next;
-        if (j + 1 < end) pg_next = lookup(j + 1);
-        const int y = (it.kvh << a.c_.page_shift) + ((j * kTileKeys + r) & (page - 1));
-#pragma unroll 1
-        for (int v = 0; v < 2; ++v) {
-          ok = __all_sync(0xffffffffu, mbar_wait_idle(&kv_empty[slot], slot_ph ^ 1, abort_flag, kDevTimeoutProducer, kWaitLimitNs));
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], L::kTile);
-          __syncwarp();
-          if (lane < copies)
-            tma_load_3d(smem + L::oKV + slot * L::kTile + half * (L::kTile / L::kHalves) + r * 128, v ? &tmV : &tmK,
-                        &kv_full[slot], 64 * half, y, pg);
-          __syncwarp();
-          if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
+        const int pg_next = j + 1 < end ? lookup(j + 1) : 0;
+        load(&tmK, j, pg);
+        if (j == it.j0) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || (x ? it.endB : it.endA) <= it.j0) continue;
+            ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[x], (qn[x] & 1) ^ 1, abort_flag, kDevTimeoutProducer));
+            if (!ok) continue;
+            ++qn[x];
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&q_full[x], a.tokens * a.group * D * 2);
+              for (int h = 0; h < L::kHalves; ++h)
+                tma_load_3d(smem + L::oQ + x * L::kTile + h * (L::kTile / L::kHalves), &tmQ, &q_full[x], 64 * h,
+                            it.kvh * a.group, it.row0 + x * a.tokens);
+            }
+            __syncwarp();
+          }
         }
+        if (ok) load(&tmV, j, pg);
+        pg = pg_next;
       }
     }
   } else if (warp == 9) {
@@ -360,60 +549,92 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           umma_bf16_ts(tmem + kO + (uint32_t)(D * x), tmem + kS + 128u * x + 8u * k, dv + (uint64_t)(128 * k), idesc_pv,
                        acc || k > 0);
       };
-      for (int i = 0; ok; ++i) {
-        if (!wait(&it_full[i & 1], (i >> 1) & 1)) break;
-        const int done = item_at(i).done, j0 = item_at(i).j0, endA = item_at(i).endA, endB = item_at(i).endB;
-        const int kv_end = item_at(i).kv_end;
-        mbar_arrive(&it_empty[i & 1]);
-        if (done) break;
-        const int end = max(endA, endB);
-        if (end <= j0) continue;
-        // scores of the first step
+      // An item's first scores are issued as soon as the previous item leaves
+      // room, in front of its other tile's last products where they can be.
+      struct Steps {
+        int done, j0, endA, endB, kv_end;
+        __device__ int last(int x) const { return x ? endB : endA; }
+        __device__ int end() const { return max(endA, endB); }
+      };
+      int n_read = 0;
+      auto read_item = [&](Steps& t) {
+        const Item& it = item_at(n_read);
+        t.done = it.done, t.j0 = it.j0, t.endA = it.endA, t.endB = it.endB, t.kv_end = it.kv_end;
+        mbar_arrive(&it_empty[n_read & 1]);
+        ++n_read;
+      };
+      auto first_scores = [&](const Steps& t, int x) {
+        ++qn[x];
+        tc_fence_after();
+        scores(x, slot);
+        umma_commit<1>(&s_full[x]);
+        if (t.j0 + 1 == t.last(x)) umma_commit<1>(&q_empty[x]);
+      };
+      Steps cur, nxt;
+      bool have = false;              // nxt holds the next item
+      bool given[2] = {false, false};  // its first scores are issued
+      while (ok) {
+        if (have) {
+          cur = nxt;
+          have = false;
+        } else {
+          if (!wait(&it_full[n_read & 1], (n_read >> 1) & 1)) break;
+          read_item(cur);
+        }
+        if (cur.done) break;
+        const int end = cur.end();
+        if (end <= cur.j0) continue;
         if (!wait(&kv_full[slot], slot_ph)) break;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int last = x ? endB : endA;
-          if (j0 >= last || !wait(&q_full[x], qn[x] & 1)) continue;
-          ++qn[x];
-          tc_fence_after();
-          scores(x, slot);
-          umma_commit<1>(&s_full[x]);
-          if (j0 + 1 == last) umma_commit<1>(&q_empty[x]);
+          if (!given[x] && cur.j0 < cur.last(x) && wait(&q_full[x], qn[x] & 1)) first_scores(cur, x);
+          given[x] = false;
         }
         if (!ok) break;
         umma_commit<1>(&kv_empty[slot]);
         next_slot();
-        for (int j = j0; j < end; ++j) {
+        for (int j = cur.j0; j < end; ++j) {
           const uint32_t vs = slot;
           if (!wait(&kv_full[slot], slot_ph)) break;
           next_slot();
           const uint32_t ks = slot;
+          bool ahead = false;  // the next item's first keys have landed
           if (j + 1 < end) {
             if (!wait(&kv_full[slot], slot_ph)) break;
             next_slot();
+          } else if (mbar_try_wait(&it_full[n_read & 1], (n_read >> 1) & 1)) {
+            read_item(nxt);
+            have = true;
+            ahead = !nxt.done && nxt.j0 < nxt.end() && mbar_try_wait(&kv_full[slot], slot_ph);
           }
-          if (kv_end - j * kTileKeys < kTileKeys) {  // values that do not exist: see the helper warp
+          if (cur.kv_end - j * kTileKeys < kTileKeys) {  // values that do not exist: see the helper warp
             clean_req[0] = (int)vs;
-            clean_req[1] = kv_end - j * kTileKeys;
+            clean_req[1] = cur.kv_end - j * kTileKeys;
             mbar_arrive(clean_ask);
             if (!wait(clean_done, cn++ & 1)) break;
           }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int last = x ? endB : endA;
-            if (j >= last || !wait(&p_half[x], pn[x] & 1)) continue;
-            tc_fence_after();
-            values(x, vs, j > j0, 0);
-            if (!wait(&p_full[x], pn[x] & 1)) continue;
-            ++pn[x];
-            tc_fence_after();
-            values(x, vs, true, 1);
-            if (j + 1 < last) {
-              scores(x, ks);
-              umma_commit<1>(&s_full[x]);
-              if (j + 2 == last) umma_commit<1>(&q_empty[x]);
-            } else {
-              umma_commit<1>(&o_full[x]);
+            const int last = cur.last(x);
+            if (j < last) {
+              if (!wait(&p_half[x], pn[x] & 1)) continue;
+              tc_fence_after();
+              values(x, vs, j > cur.j0, 0);
+              if (!wait(&p_full[x], pn[x] & 1)) continue;
+              ++pn[x];
+              tc_fence_after();
+              values(x, vs, true, 1);
+              if (j + 1 < last) {
+                scores(x, ks);
+                umma_commit<1>(&s_full[x]);
+                if (j + 2 == last) umma_commit<1>(&q_empty[x]);
+              } else {
+                umma_commit<1>(&o_full[x]);
+              }
+            }
+            if (ahead && nxt.j0 < nxt.last(x) && mbar_try_wait(&q_full[x], qn[x] & 1)) {
+              first_scores(nxt, x);
+              given[x] = true;
             }
           }
           if (!ok) break;
@@ -457,11 +678,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // Decodes the CTA's work items ahead of their use.
     grid_dep_wait();
     grid_dep_launch();
+    ShareWalk walk;
+    Pairs mine = {0, 0, 0, 0, 0};
+    if (a.shares) walk.init(a, lane);
+    else if (a.b.batch <= 32) mine = load_pairs(a, lane);
     for (int i = 0;; ++i) {
       Item it;
-      // every other round backwards: the items come in falling cost, so that
-      // each CTA's sum stays near the mean
-      decode_item(a, i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, it);
+      it.done = 1;
+      if (a.shares) {
+        if (!walk.next(a, it)) it.done = 1;
+      } else {
+        // every other round backwards: the items come in falling cost, so that
+        // each CTA's sum stays near the mean
+        ranked_item(a, mine, i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, it);
+      }
       if (!__all_sync(0xffffffffu, mbar_wait_idle(&it_empty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag,
                                                   kDevTimeoutProducer, 100 * kWaitLimitNs)))
         break;
@@ -505,78 +735,68 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // weights: held in registers in between, they left too few for the
         // exponentials' temporaries (spills; 750 cycles per 64 keys, not 560).
         const int base = j * kTileKeys;
-        auto step = [&](auto edge_tag) {
-          constexpr bool kEdge = decltype(edge_tag)::value;
-          auto mask = [&](uint32_t(&r)[32], int q) {
-            if (kEdge && base + 32 * q + 32 > warp_lim) {
+        auto mask = [&](uint32_t(&r)[32], int c0) {  // scores of columns c0 ... c0 + 31
+          if (base + c0 + 32 > warp_lim) {
+            const int left = lim - base - c0;
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (base + 32 * q + e >= lim) r[e] = 0xff800000u;  // -inf
-            }
-          };
-          float mx[2];
-          {
-            uint32_t r[4][32];
-            tmem_ld_32x32b_x32(tS, r[0]);
-            tmem_ld_32x32b_x32(tS + 32u, r[1]);
-            tmem_ld_wait_regs(r[0]);
-            tmem_ld_wait_regs(r[1]);
-            tmem_ld_32x32b_x32(tS + 64u, r[2]);
-            tmem_ld_32x32b_x32(tS + 96u, r[3]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (q == 2) {
-                tmem_ld_wait_regs(r[2]);
-                tmem_ld_wait_regs(r[3]);
-              }
-              mask(r[q], q);
-              if (q == 0) {
-                mx[0] = __uint_as_float(r[0][0]);
-                mx[1] = __uint_as_float(r[0][1]);
-              }
-#pragma unroll
-              for (int e = q ? 0 : 2; e < 30; e += 4) {
-                mx[0] = max3(mx[0], __uint_as_float(r[q][e]), __uint_as_float(r[q][e + 1]));
-                mx[1] = max3(mx[1], __uint_as_float(r[q][e + 2]), __uint_as_float(r[q][e + 3]));
-              }
-              if (q == 0) mx[0] = max3(mx[0], __uint_as_float(r[0][30]), __uint_as_float(r[0][31]));
-            }
+            for (int e = 0; e < 32; ++e)
+              if (e >= left) r[e] = 0xff800000u;  // -inf
           }
-          uint32_t s[2][32];
-          tmem_ld_32x32b_x32(tS, s[0]);
-          const float cand = fmaxf(mx[0], mx[1]) * a.c;
-          // the maximum in use follows only when it falls behind by 2^8: weights
-          // up to 2^8 cost nothing in bf16 or fp32, and most steps leave O alone
-          const bool grow = valid && cand > mc + kLazyMax;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = grow ? ex2(mc - cand) : 1.0f;
-            if (grow) {
-              mc = cand;
-              l *= f;
-            }
-            if (j > it.j0) {
+        };
+        float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll 1
-              for (int q = 0; q < D / 16; ++q) {
-                uint32_t o[16];
-                tmem_ld_32x32b_x16(tO + 16u * q, o);
-                tmem_ld_wait_regs(o);
+        for (int c0 = 0; c0 < 128; c0 += 64) {
+          uint32_t r[2][32];
+          tmem_ld_32x32b_x32(tS + c0, r[0]);
+          tmem_ld_32x32b_x32(tS + c0 + 32, r[1]);
+          tmem_ld_wait_regs(r[0]);
+          tmem_ld_wait_regs(r[1]);
+          mask(r[0], c0);
+          mask(r[1], c0 + 32);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st_32x32b_x16(tO + 16u * q, o);
-              }
+          for (int e = 0; e < 32; e += 2) {
+            mx0 = max3(mx0, __uint_as_float(r[0][e]), __uint_as_float(r[0][e + 1]));
+            mx1 = max3(mx1, __uint_as_float(r[1][e]), __uint_as_float(r[1][e + 1]));
+          }
+        }
+        const float cand = fmaxf(mx0, mx1) * a.c;
+        // the maximum in use follows only when it falls behind by 2^8: weights
+        // up to 2^8 cost nothing in bf16 or fp32, and most steps leave O alone
+        const bool grow = valid && cand > mc + kLazyMax;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? ex2(mc - cand) : 1.0f;
+          if (grow) {
+            mc = cand;
+            l *= f;
+          }
+          if (j > it.j0) {
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(tO + 16u * q, o);
+              tmem_ld_wait_regs(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x16(tO + 16u * q, o);
             }
           }
-          const float sub = mc == -INFINITY ? 0.f : -mc;
-          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+        }
+        const float sub = mc == -INFINITY ? 0.f : -mc;
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 64) {
+          uint32_t s[2][32];
+          tmem_ld_32x32b_x32(tS + c0, s[0]);
+          tmem_ld_32x32b_x32(tS + c0 + 32, s[1]);
+          tmem_ld_wait_regs(s[0]);
+          tmem_ld_wait_regs(s[1]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            tmem_ld_wait_regs(s[q & 1]);
-            if (q < 3) tmem_ld_32x32b_x32(tS + 32u * (q + 1), s[(q + 1) & 1]);
-            mask(s[q & 1], q);
+          for (int q = 0; q < 2; ++q) {
+            mask(s[q], c0 + 32 * q);
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float2 s2 = make_float2(__uint_as_float(s[q & 1][2 * e]), __uint_as_float(s[q & 1][2 * e + 1]));
+              const float2 s2 = make_float2(__uint_as_float(s[q][2 * e]), __uint_as_float(s[q][2 * e + 1]));
               const float2 y = fma2(s2, make_float2(a.c, a.c), make_float2(sub, sub));
               // the XU pipe's 16 exponentials a cycle would bound the kernel: part
               // of them is computed on the FMA pipe
@@ -586,19 +806,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
               w[e] = reinterpret_cast<const uint32_t&>(h);
             }
-            // columns 16 q ... of weights lie on scores that have been read
-            tmem_st_32x32b_x16(tS + 16u * q, w);
-            if (q & 1) {  // half of the keys: their product may start
-              tmem_st_wait();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(q == 1 ? &p_half[x] : &p_full[x]);
-            }
+            // weights of columns c take columns c / 2, whose scores have been read
+            tmem_st_32x32b_x16(tS + (c0 >> 1) + 16u * q, w);
           }
-          l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-        };
-        if (base + kTileKeys > warp_lim) step(std::true_type{});
-        else step(std::false_type{});
+          // half of the keys: their product may start
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(c0 == 0 ? &p_half[x] : &p_full[x]);
+        }
+        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
       }
       if (!ok) break;
       // -------------------------------------------------------- epilogue
@@ -610,29 +827,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       const float inv = l > 0.f ? 1.0f / l : 0.f;
       const int h = it.kvh * a.group + head;
-      if (a.po != nullptr) {
-        const long long at = ((long long)it.split * a.T + t) * a.n_heads + h;
+      uint8_t* stage = smem + L::oStage + warp * 4096;
+      if (it.slot >= 0) {
+        const long long at = (long long)it.slot * 256 + 128 * x + row;
         if (valid) a.plse[at] = l > 0.f ? mc + log2f(l) : -INFINITY;
+        const bool write = valid && l > 0.f;
+        const uint32_t writes = __ballot_sync(0xffffffffu, write);
         if (any) {
 #pragma unroll 1
           for (int q = 0; q < D / 32; ++q) {
             uint32_t o[32];
             tmem_ld_32x32b_x32(tO + 32u * q, o);
             tmem_ld_wait_regs(o);
-            if (valid && l > 0.f) {
-              float4* dst = reinterpret_cast<float4*>(a.po + at * D + 32 * q);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                                     __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                  make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                              __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+            __syncwarp();
+            float* dst = a.po + (at - lane) * D + 32 * q + 4 * (lane & 7);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int rr = 4 * e + (lane >> 3);
+              if (writes >> rr & 1)
+                *reinterpret_cast<float4*>(dst + rr * D) =
+                    *reinterpret_cast<const float4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
             }
+            __syncwarp();
           }
         }
       } else {
         // 64 columns at a time through the warp's 4 KB of shared memory, so that
         // rows leave as whole 128-byte lines (16-byte chunks swizzled by the row)
         __nv_bfloat16* dst = valid ? a.o + (long long)t * a.ldo + (long long)h * D : nullptr;
-        uint8_t* stage = smem + L::oStage + warp * 4096;
 #pragma unroll 1
         for (int q = 0; q < D / 64; ++q) {
           uint32_t o[2][32];
@@ -688,60 +915,113 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-// Joins partial outputs: O = sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M).
-// One warp per (row, head); a lane holds one split's weight (splits <= 64).
+// Joins the parts of items that shares cut:
+//   O = sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M),  s in share order.
+// One CTA per tile pair, kv head and 32 rows; 4 rows per warp.
 template <int D>
-__global__ void __launch_bounds__(128) k_merge(const float* po, const float* plse, int splits, int T, int n_heads,
-                                               const int32_t* cu_q, int batch, __nv_bfloat16* o, long long ldo) {
-  const int lane = threadIdx.x & 31;
-  const long long rows = (long long)T * n_heads;
-  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  grid_dep_wait();
-  if (r >= rows) return;
-  const int t = (int)(r / n_heads), h = (int)(r % n_heads);
-  const float ls0 = lane < splits ? plse[lane * rows + r] : -INFINITY;
-  const float ls1 = lane + 32 < splits ? plse[(lane + 32) * rows + r] : -INFINITY;
-  if (t < cu_q[0] || t >= cu_q[batch]) return;
-  float m = fmaxf(ls0, ls1);
+__global__ void __launch_bounds__(256) k_merge(const TcArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // lengths and offsets are inputs of the call: k_attn lets this grid start
+  // only after its own wait, so they are complete here
+  const int pair = 2 * a.tokens, heads = a.c_.n_kv_heads, kvh = blockIdx.y;
+  int seq = -1, tile = blockIdx.x;
+  for (int b0 = 0; b0 < a.b.batch; b0 += 32) {
+    const Pairs p = load_pairs(a, b0 + lane);
+    int incl = p.np;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  const float w0 = ls0 == -INFINITY ? 0.f : ex2(ls0 - m), w1 = ls1 == -INFINITY ? 0.f : ex2(ls1 - m);
-  float z = w0 + w1;
-#pragma unroll
-  for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-  constexpr int E = D / 32;
-  float acc[E] = {};
-#pragma unroll 8
-  for (int s = 0; s < splits; ++s) {
-    const float w = __shfl_sync(0xffffffffu, s < 32 ? w0 : w1, s & 31);
-    if (w != 0.f) {  // an empty part's row is not written
-      const float* src = po + (s * rows + r) * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += w * src[e];
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
     }
+    const uint32_t hit = __ballot_sync(0xffffffffu, tile < incl);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      seq = b0 + src;
+      tile -= __shfl_sync(0xffffffffu, incl - p.np, src);
+      break;
+    }
+    tile -= __shfl_sync(0xffffffffu, incl, 31);
   }
-  const float inv = z > 0.f ? 1.f / z : 0.f;
-  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(o + t * ldo + (long long)h * D + lane * E);
+  grid_dep_wait();
+  if (seq < 0) return;
+  const Pairs s = load_pairs(a, seq);
+  long long before, total;
+  share_sums(a, seq, lane, before, total);
+  const Measure m = measure(a, s);
+  const long long s0 = before * heads + kvh * m.before(s.np) + m.before(tile), size = m.of(tile);
+  total *= heads;
+  const int steps = pair_steps(s, tile, pair);
+  const int c0 = (int)(((s0 + 1) * a.shares - 1) / total), c1 = (int)(((s0 + size) * a.shares - 1) / total);
+  // slot of share c's part; -1: no step of the item, -2: all of them
+  auto part = [&](int c) {
+    if (c > c1) return -1;
+    const long long lo = max(0ll, total * c / a.shares - s0), hi = min(size, total * (c + 1) / a.shares - s0);
+    if (lo >= hi) return -1;
+    const int slo = (int)min((long long)steps, lo / kTileKeys);
+    const int shi = hi == size ? steps : (int)min((long long)steps, hi / kTileKeys);
+    return slo >= shi ? -1 : slo == 0 && shi == steps ? -2 : lo > 0 ? 2 * c : 2 * c + 1;
+  };
+  bool whole = steps == 0;
+  for (int c = c0 + lane; c <= c1; c += 32) whole |= part(c) == -2;
+  if (__any_sync(0xffffffffu, whole)) return;  // finished by its CTA
+  constexpr int E = D / 32;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const int r = blockIdx.z * 32 + warp * 4 + i;  // row of the pair
+    const int x = r >> 7, tok = (r & 127) / a.group, ti = x * a.tokens + tok;
+    const int t = s.first + tile * pair + ti;
+    if (tok >= a.tokens || ti >= min(pair, s.n - tile * pair) || t < 0 || t >= a.T) continue;
+    const int h = kvh * a.group + (r & 127) - tok * a.group;
+    float acc[E] = {}, z = 0.f, top = -INFINITY;
+    for (int b0 = c0; b0 <= c1; b0 += 32) {
+      const int slot = part(b0 + lane);
+      const float lse = slot >= 0 ? a.plse[(long long)slot * 256 + r] : -INFINITY;
+      float mx = lse;
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e) dst[e] = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      if (mx == -INFINITY) continue;
+      const float mn = fmaxf(top, mx), f = ex2(top - mn);
+      top = mn;
+      const float w = lse == -INFINITY ? 0.f : ex2(lse - mn);
+      float zz = w;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) zz += __shfl_xor_sync(0xffffffffu, zz, d);
+      z = z * f + zz;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= f;
+      const int cnt = min(32, c1 - b0 + 1);
+#pragma unroll 4
+      for (int k = 0; k < cnt; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const int sk = __shfl_sync(0xffffffffu, slot, k);
+        if (wk != 0.f) {  // an empty part's row is not written
+          const float* src = a.po + ((long long)sk * 256 + r) * D + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += wk * src[e];
+        }
+      }
+    }
+    const float inv = z > 0.f ? 1.f / z : 0.f;
+    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + t * a.ldo + (long long)h * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) dst[e] = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  }
 }
 
-// Work split of a call with at most `pairs` tile pairs per kv head: enough key
-// splits to fill the SMs, none shorter than 512 keys.
-inline int tc_splits(long long pairs, int n_kv_heads, long long max_kv, int sms) {
-  const long long items = pairs * n_kv_heads;
-  const long long steps = (max_kv + kTileKeys - 1) / kTileKeys;
-  return (int)std::max(1ll, std::min({sms / std::max(1ll, items), steps / 4, 64ll}));
+// Shares of a call whose work is at most `items` tile pairs times kv heads of
+// `keys` keys: as many CTAs as there are SMs, none for less than 512 keys.
+inline int tc_shares(long long items, long long keys, int sms) {
+  return (int)std::max(1ll, std::min<long long>(sms, items * ((keys + 511) / 512)));
 }
 
 template <int D>
 inline cudaError_t launch_tc(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const TcArgs& a,
-                             long long items, int sms, cudaStream_t st) {
+                             int ctas, cudaStream_t st) {
   auto kern = k_attn<D>;
   const cudaError_t e = smem_limit(reinterpret_cast<const void*>(kern), TcLayout<D>::kAlloc);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<long long>(items, sms));
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kTcThreads);
   cfg.dynamicSmemBytes = TcLayout<D>::kAlloc;
   cfg.stream = st;
@@ -754,18 +1034,17 @@ inline cudaError_t launch_tc(const CUtensorMap& tmQ, const CUtensorMap& tmK, con
 }
 
 template <int D>
-inline cudaError_t launch_merge(const float* po, const float* plse, int splits, int T, int n_heads, const int32_t* cu_q,
-                                int batch, __nv_bfloat16* o, long long ldo, cudaStream_t st) {
+inline cudaError_t launch_merge(const TcArgs& a, int pairs, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((long long)T * n_heads + 3) / 4));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(pairs, a.c_.n_kv_heads, 8);
+  cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_merge<D>, po, plse, splits, T, n_heads, cu_q, batch, o, ldo);
+  return cudaLaunchKernelEx(&cfg, k_merge<D>, a);
 }
 
 }  // namespace attn

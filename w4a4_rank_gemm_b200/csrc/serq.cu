@@ -2032,9 +2032,14 @@ serq_status check_ws(const void* ws, size_t have, size_t need) {
 
 namespace {
 
-// Tile pairs per kv head that a prompt call can have at most, and its key splits.
+// Tile pairs per kv head that a prompt call can have at most, its work split
+// and workspace.  Whole items balance well once there are two per SM; with
+// fewer, equal shares do (whose cut items cost a pass to join them): below one
+// item per SM always, up to two where the keys reach far in front of the rows,
+// so that all items cost about the same (256 items of prompts of 2048 tokens
+// pack to within 3% of the mean as they are).
 struct PrefillPlan {
-  int group, tokens, splits;
+  int group, tokens, shares, ctas;
   long long pairs;
   size_t ws;
 };
@@ -2043,9 +2048,12 @@ PrefillPlan prefill_plan(const serq_kv_cache* c, int T, int n_heads, int batch, 
   p.group = n_heads / c->n_kv_heads;
   p.tokens = serq::attn::kTileRows / p.group;
   p.pairs = T / (2 * p.tokens) + std::min(batch, T);
-  const long long cap = (long long)max_pages * c->page_size;
-  p.splits = serq::attn::tc_splits(p.pairs, c->n_kv_heads, max_kv ? std::min<long long>(max_kv, cap) : cap, sm_count());
-  p.ws = p.splits > 1 ? (size_t)p.splits * T * n_heads * (c->head_dim + 1) * sizeof(float) : 0;
+  const long long cap = (long long)max_pages * c->page_size, items = p.pairs * c->n_kv_heads, sms = sm_count();
+  const long long keys = max_kv ? std::min<long long>(max_kv, cap) : cap;
+  const bool share = keys > 512 && (items < sms || (items < 2 * sms && keys * batch >= 3ll * T));
+  p.shares = share ? serq::attn::tc_shares(items, keys, (int)sms) : 0;
+  p.ctas = share ? p.shares : (int)std::min(items, sms);
+  p.ws = (size_t)2 * p.shares * 256 * (c->head_dim + 1) * sizeof(float);
   return p;
 }
 
@@ -2083,25 +2091,23 @@ serq_status serq_attn_prefill(const serq_kv_cache* cache, const void* Q, int ldq
   serq::attn::TcArgs a;
   a.o = static_cast<__nv_bfloat16*>(O);
   a.ldo = ldo;
-  a.po = p.ws ? static_cast<float*>(ws) : nullptr;
-  a.plse = p.ws ? a.po + (size_t)p.splits * T * n_heads * D : nullptr;
+  a.po = static_cast<float*>(ws);
+  a.plse = p.shares ? a.po + (size_t)2 * p.shares * 256 * D : nullptr;
   a.c = attn_scale(scale);
   a.neg = scale < 0.f;
   a.T = T;
   a.n_heads = n_heads;
   a.group = p.group;
   a.tokens = p.tokens;
-  a.splits = p.splits;
+  a.shares = p.shares;
   a.prefix = 0;
   a.b = {cu_q, kv_len, page_table, batch, max_pages, ld_table};
   a.c_ = cache_args(cache);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const long long items = p.pairs * cache->n_kv_heads * p.splits;
-  cudaError_t e = D == 128 ? serq::attn::launch_tc<128>(tmQ, cache->tm[0][0], cache->tm[1][0], a, items, sm_count(), st)
-                           : serq::attn::launch_tc<64>(tmQ, cache->tm[0][0], cache->tm[1][0], a, items, sm_count(), st);
-  if (e == cudaSuccess && p.ws)
-    e = D == 128 ? serq::attn::launch_merge<128>(a.po, a.plse, p.splits, T, n_heads, cu_q, batch, a.o, ldo, st)
-                 : serq::attn::launch_merge<64>(a.po, a.plse, p.splits, T, n_heads, cu_q, batch, a.o, ldo, st);
+  cudaError_t e = D == 128 ? serq::attn::launch_tc<128>(tmQ, cache->tm[0][0], cache->tm[1][0], a, p.ctas, st)
+                           : serq::attn::launch_tc<64>(tmQ, cache->tm[0][0], cache->tm[1][0], a, p.ctas, st);
+  if (e == cudaSuccess && p.shares)
+    e = D == 128 ? serq::attn::launch_merge<128>(a, (int)p.pairs, st) : serq::attn::launch_merge<64>(a, (int)p.pairs, st);
   if (e != cudaSuccess) return cuda_fail(e, "serq_attn_prefill launch");
   return ok();
 }
@@ -2113,9 +2119,8 @@ namespace {
 // Work split and workspace of a decode call.
 struct DecodePlan {
   int group, row_blocks, rows, shares;
-  int prefix, tokens, psplits;  // the shared prefix's pass, when prefix > 0
-  long long pairs;
-  size_t slots, ws;
+  int prefix, tokens, pshares;  // the shared prefix's pass, when prefix > 0
+  size_t slots, pslots, ws;
 };
 DecodePlan decode_plan(const serq_kv_cache* c, int batch, int n_heads, int max_pages, int prefix_len, int max_kv) {
   DecodePlan p = {};
@@ -2131,10 +2136,11 @@ DecodePlan decode_plan(const serq_kv_cache* c, int batch, int n_heads, int max_p
   if (p.prefix) {
     p.slots += (size_t)batch * c->n_kv_heads * p.row_blocks;
     p.tokens = serq::attn::kTileRows / p.group;
-    p.pairs = (batch + 2 * p.tokens - 1) / (2 * p.tokens);
-    p.psplits = serq::attn::tc_splits(p.pairs, c->n_kv_heads, p.prefix, sm_count());
+    const long long items = (long long)(batch + 2 * p.tokens - 1) / (2 * p.tokens) * c->n_kv_heads;
+    p.pshares = serq::attn::tc_shares(items, p.prefix, sm_count());
+    p.pslots = 2 * (size_t)p.pshares + items;
   }
-  p.ws = (p.slots * p.rows + (size_t)p.psplits * batch * n_heads) * (c->head_dim + 1) * sizeof(float);
+  p.ws = (p.slots * p.rows + p.pslots * 256) * (c->head_dim + 1) * sizeof(float);
   return p;
 }
 
@@ -2179,14 +2185,15 @@ serq_status serq_attn_decode(const serq_kv_cache* cache, const void* Q, int ldq,
   d.b = {nullptr, kv_len, page_table, batch, max_pages, ld_table};
   d.c_ = cache_args(cache);
   // workspace: slot outputs, prefix outputs, then the log-sums of both
-  const size_t n_slot = p.slots * p.rows, n_pre = (size_t)p.psplits * batch * n_heads;
+  const size_t n_slot = p.slots * p.rows, n_pre = p.pslots * 256;
   d.so = static_cast<float*>(ws);
   float* po = d.so + n_slot * D;
   d.slse = po + n_pre * D;
   float* plse = d.slse + n_slot;
   d.po = po;
   d.plse = plse;
-  d.psplits = p.psplits;
+  d.ptokens = p.tokens;
+  d.pshares = p.pshares;
   cudaError_t e = cudaSuccess;
   if (p.prefix) {
     CUtensorMap tmQ;
@@ -2201,13 +2208,12 @@ serq_status serq_attn_decode(const serq_kv_cache* cache, const void* Q, int ldq,
     a.n_heads = n_heads;
     a.group = p.group;
     a.tokens = p.tokens;
-    a.splits = p.psplits;
+    a.shares = p.pshares;
     a.prefix = p.prefix;
     a.b = d.b;
     a.c_ = d.c_;
-    const long long items = p.pairs * cache->n_kv_heads * p.psplits;
-    e = D == 128 ? serq::attn::launch_tc<128>(tmQ, cache->tm[0][0], cache->tm[1][0], a, items, sm_count(), st)
-                 : serq::attn::launch_tc<64>(tmQ, cache->tm[0][0], cache->tm[1][0], a, items, sm_count(), st);
+    e = D == 128 ? serq::attn::launch_tc<128>(tmQ, cache->tm[0][0], cache->tm[1][0], a, p.pshares, st)
+                 : serq::attn::launch_tc<64>(tmQ, cache->tm[0][0], cache->tm[1][0], a, p.pshares, st);
   }
   if (e == cudaSuccess)
     e = D == 128 ? serq::attn::launch_decode<128>(cache->tm[0][1], cache->tm[1][1], d, st)
