@@ -37,7 +37,7 @@ constexpr int kTileKeys = 128;  // keys of a step
 constexpr int kTcThreads = 384;
 constexpr int kRegsIssue = 88, kRegsSoftmax = 208;
 static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= kTcThreads * 168, "register split");
-constexpr int kFmaPairs = 6;  // of 16 pairs of exponentials, how many go to the FMA pipe
+constexpr int kFmaPairs = 4;  // of 16 pairs of exponentials, how many go to the FMA pipe
 constexpr float kLazyMax = 8.0f;  // log2: how far a row's scores may exceed the maximum in use
 
 struct TcArgs {
@@ -358,8 +358,8 @@ struct ShareWalk {
       if (emit) {
         fill_item(a, s, seq, tile, kvh, slo, shi, it);
         it.slot = a.prefix == 0 && slo == 0 && shi == steps ? -1
-                  : lo > 0                                  ? 2 * blockIdx.x
-                  : hi < size                               ? 2 * blockIdx.x + 1
+                  : lo > 0                                  ? 2 * (int)blockIdx.x
+                  : hi < size                               ? 2 * (int)blockIdx.x + 1
                                                             : 2 * a.shares + kvh * s.np + tile;
       }
       x = start + hi;
