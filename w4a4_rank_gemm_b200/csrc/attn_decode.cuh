@@ -50,8 +50,8 @@ struct DecLayout {
   static constexpr int kOperand = kBlockKeys * D * 2;  // bytes of a block's K or V
   static constexpr int kSlots = D == 128 ? 6 : 12;     // even: a slot is always the same warps'
   static constexpr int oRing = 0;
-  static constexpr int oMerge = kSlots * 2 * kOperand;  // [4][16][D] floats, rows turned by 8 columns each
-  static constexpr int oStat = oMerge + 4 * 16 * D * 4;  // m and l: [2][8][16] floats
+  static constexpr int oMerge = kSlots * 2 * kOperand;  // 64 D floats
+  static constexpr int oStat = oMerge + 64 * D * 4;      // m and l: [2][8][16] floats
   static constexpr int oBar = oStat + 2 * 8 * 16 * 4;
   static constexpr int oMisc = oBar + 2 * kSlots * 8;
   static constexpr int kAlloc = oMisc + 16 + 1024;
@@ -64,55 +64,85 @@ __device__ __forceinline__ int dec_blocks(const DecArgs& a, int b) {
   return ceil_div(max(0, min(a.b.kv_len[b], cap) - a.prefix), kBlockKeys);
 }
 
-// Sum of the sequences' blocks, all of them and those before b (the warp calls).
-__device__ __forceinline__ void dec_sums(const DecArgs& a, int b, int lane, long long& before, long long& total) {
-  long long lo = 0, all = 0;
-  for (int i = lane; i < a.b.batch; i += 32) {
-    const int n = dec_blocks(a, i);
-    all += n;
-    if (i < b) lo += n;
-  }
+// Warp sum of non-negative counts; `small`: it stays below 2^31.
+__device__ __forceinline__ long long warp_sum(long long v, bool small) {
+  if (small) return __reduce_add_sync(0xffffffffu, (uint32_t)v);
 #pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    lo += __shfl_xor_sync(0xffffffffu, lo, d);
-    all += __shfl_xor_sync(0xffffffffu, all, d);
-  }
-  before = lo;
-  total = all;
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
 }
+
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// Equal shares of `total` blocks: the first total % G have one block more.
+struct Shares {
+  long long base, more;  // blocks of a share, shares with one more
+  __device__ Shares(long long total, int g) {
+    base = quotient(total, g);
+    more = total - base * g;
+  }
+  __device__ long long start(long long c) const { return c * base + min(c, more); }
+  __device__ int of(long long w) const {  // the share that holds block w
+    const long long m = more * (base + 1);
+    return (int)(w < m ? quotient(w, base + 1) : more + quotient(w - m, base));
+  }
+};
 
 // Position in the batch's run of blocks.
 struct DecPos {
   int b, h, blk, nb;  // sequence, head block, next block, blocks of the sequence
 };
 
-// The place of block w (the warp calls).  w < total * heads.
-__device__ __forceinline__ DecPos dec_find(const DecArgs& a, long long w, int heads, int lane) {
-  long long done = 0;
-  for (int b0 = 0; b0 < a.b.batch; b0 += 32) {
-    const int b = b0 + lane;
-    const int nb = b < a.b.batch ? dec_blocks(a, b) : 0;
-    long long incl = nb;
+// Finds a share's beginning.  Lane i counts the blocks of sequences
+// [i q, (i + 1) q), q = ceil(batch / 32), in one round of loads.
+struct DecFind {
+  int q;
+  long long mine, upto, total;  // of the lane's sequences, of them and those before, of all
+  __device__ DecFind(const DecArgs& a, int lane) {
+    q = ceil_div(a.b.batch, 32);
+    mine = 0;
+#pragma unroll 4
+    for (int i = 0; i < q; ++i) {
+      const int b = lane * q + i;
+      if (b < a.b.batch) mine += dec_blocks(a, b);
+    }
+    upto = mine;
+    if (a.b.batch <= 32) {  // fewer than 2^26 blocks each
+      int v = (int)mine;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += v;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
+      }
+      upto = v;
+      total = __shfl_sync(0xffffffffu, v, 31);
+    } else {
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+      }
+      total = __shfl_sync(0xffffffffu, upto, 31);
     }
-    const uint32_t hit = __ballot_sync(0xffffffffu, w < (done + incl) * heads);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      DecPos p;
-      p.b = b0 + src;
-      p.nb = __shfl_sync(0xffffffffu, nb, src);
-      const long long rest = w - (done + __shfl_sync(0xffffffffu, incl, src) - p.nb) * heads;
-      p.h = (int)(rest / p.nb);
-      p.blk = (int)(rest - (long long)p.h * p.nb);
-      return p;
-    }
-    done += __shfl_sync(0xffffffffu, incl, 31);
   }
-  return DecPos{0, 0, 0, 1};
-}
+  // The place of block w < total * heads (the warp calls).
+  __device__ DecPos find(const DecArgs& a, long long w, int heads) const {
+    const int src = __ffs(__ballot_sync(0xffffffffu, w < upto * heads)) - 1;
+    long long rest = w - __shfl_sync(0xffffffffu, upto - mine, src) * heads;
+    DecPos p;
+    p.b = src * q;
+    for (;; ++p.b) {
+      p.nb = dec_blocks(a, p.b);
+      if (rest < (long long)p.nb * heads) break;
+      rest -= (long long)p.nb * heads;
+    }
+    p.h = (int)quotient(rest, p.nb);
+    p.blk = (int)(rest - (long long)p.h * p.nb);
+    return p;
+  }
+};
 
 __device__ __forceinline__ void dec_next_pair(const DecArgs& a, DecPos& p, int heads) {
   p.blk = 0;
@@ -174,62 +204,92 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   grid_dep_launch();
 
   const int heads = a.c_.n_kv_heads * a.row_blocks;
-  long long before, total;
-  dec_sums(a, 0, lane, before, total);
-  total *= heads;
-  const long long w0 = total * blockIdx.x / a.shares, w1 = total * (blockIdx.x + 1) / a.shares;
+  const DecFind batch(a, lane);
+  const Shares shares(batch.total * heads, a.shares);
+  const long long w0 = shares.start(blockIdx.x), w1 = shares.start(blockIdx.x + 1);
   const int cap = a.b.max_pages << a.c_.page_shift;
+  // keys of a copy: a block's K or V lie in shared memory as box rows of its
+  // first 64 columns, the same rows of the next 64, then the next box
+  const int box = min(1 << a.c_.page_shift, kBlockKeys);
   DecPos p = {};
-  if (w0 < w1) p = dec_find(a, w0, heads, lane);
+  if (w0 < w1) p = batch.find(a, w0, heads);
 
   if (warp == 8) {
     if (lane == 0) {
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
     }
+    // The pages of up to 32 copies (8 to 32 blocks of one pair) are looked up
+    // at once, one such batch ahead of the copies: a lookup costs a trip to L2,
+    // about as long as a block takes.
     const int page = 1 << a.c_.page_shift;
-    const int box = min(page, kBlockKeys);
-    const int copies = kBlockKeys / box * L::kHalves;  // per operand
-    const int half = lane & (L::kHalves - 1), r = (lane / L::kHalves) * box;
-    // page of this lane's copy in the block at position p
-    auto lookup = [&](const DecPos& at) {
-      const int key = a.prefix + at.blk * kBlockKeys + r;
+    const int per_block = kBlockKeys / box, max_n = 32 / per_block;
+    auto lookup = [&](const DecPos& at, int n) {
+      const int key = a.prefix + at.blk * kBlockKeys + lane * box;
       int pg = a.c_.n_pages;  // outside the map: filled with zeros
-      if (lane < copies && key < min(a.b.kv_len[at.b], cap)) {
+      if (lane < n * per_block && key < min(a.b.kv_len[at.b], cap)) {
         const int e = a.b.table[(long long)at.b * a.b.ldt + (key >> a.c_.page_shift)];
         if (e >= 0 && e < a.c_.n_pages) pg = e;
         else note_bad_page();
       }
       return pg;
     };
-    int pg = w0 < w1 ? lookup(p) : 0;
     uint32_t slot = 0, ph = 0;
-    for (long long w = w0; w < w1; ++w) {
+    bool ok = true;
+    long long w = w0;
+    int n = (int)min(min((long long)(p.nb - p.blk), w1 - w), (long long)max_n);
+    int pg = w < w1 ? lookup(p, n) : 0;
+    while (w < w1 && ok) {
       const DecPos cur = p;
-      const int cur_pg = pg;
-      if (++p.blk == p.nb) dec_next_pair(a, p, heads);
-      if (w + 1 < w1) pg = lookup(p);  // one block ahead of its copy
-      if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ph ^ 1, abort_flag, kDevTimeoutProducer))) break;
-      if (lane == 0) mbar_arrive_expect_tx(&full[slot], 2 * L::kOperand);
-      __syncwarp();
-      if (lane < copies) {
-        const int key = a.prefix + cur.blk * kBlockKeys + r;
-        const int y = ((cur.h / a.row_blocks) << a.c_.page_shift) + (key & (page - 1));
-        uint8_t* dst = smem + L::oRing + slot * 2 * L::kOperand + half * (kBlockKeys * 128) + r * 128;
-        tma_load_3d(dst, &tmK, &full[slot], 64 * half, y, cur_pg);
-        tma_load_3d(dst + L::kOperand, &tmV, &full[slot], 64 * half, y, cur_pg);
+      const int cur_n = n, cur_pg = pg;
+      w += n;
+      p.blk += n;
+      if (p.blk == p.nb) dec_next_pair(a, p, heads);
+      n = (int)min(min((long long)(p.nb - p.blk), w1 - w), (long long)max_n);
+      if (w < w1) pg = lookup(p, n);
+      const int y0 = ((cur.h / a.row_blocks) << a.c_.page_shift);
+      for (int i = 0; i < cur_n; ++i) {
+        const int at_pg = __shfl_sync(0xffffffffu, cur_pg, (i * per_block + lane) & 31);  // lane: copy within the block
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], ph ^ 1, abort_flag, kDevTimeoutProducer));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], 2 * L::kOperand);
+        __syncwarp();
+        if (lane < per_block) {
+          const int key = a.prefix + (cur.blk + i) * kBlockKeys + lane * box;
+          const int y = y0 + (key & (page - 1));
+          uint8_t* dst = smem + L::oRing + slot * 2 * L::kOperand + lane * box * (2 * D);
+          tma_load_4d(dst, &tmK, &full[slot], 0, y, 0, at_pg);
+          tma_load_4d(dst + L::kOperand, &tmV, &full[slot], 0, y, 0, at_pg);
+        }
+        __syncwarp();
+        if (++slot == L::kSlots) slot = 0, ph ^= 1;
       }
-      __syncwarp();
-      if (++slot == L::kSlots) slot = 0, ph ^= 1;
     }
   } else {
     const int wg = warp >> 2, kq = (warp & 3) * 16;  // this warp's keys of a block
     const int quad = lane >> 2, qc = (lane & 3) * 2;
+    const int in_box = kq & (box - 1), box_at = (kq - in_box) * (2 * D), half_at = box * 128;
     bool ok = true;
     float* merge = reinterpret_cast<float*>(smem + L::oMerge);
     float* st_m = reinterpret_cast<float*>(smem + L::oStat);
     float* st_l = st_m + 8 * 16;
     uint32_t it = 0;  // blocks since the share's first
+    // the query fragments of the pair at position `at`
+    auto load_q = [&](const DecPos& at, uint32_t(&f)[D / 16][4]) {
+      const int kvh = at.h / a.row_blocks, rb = at.h - kvh * a.row_blocks, nrows = a.group - 16 * rb;
+      const __nv_bfloat16* q0 = a.q + at.b * a.ldq + (long long)(kvh * a.group + 16 * rb + quad) * D + qc;
+      const __nv_bfloat16* q1 = q0 + 8 * D;
+      const bool v0 = quad < nrows, v1 = quad + 8 < nrows;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        f[k][0] = v0 ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k) : 0u;
+        f[k][1] = v1 ? *reinterpret_cast<const uint32_t*>(q1 + 16 * k) : 0u;
+        f[k][2] = v0 ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k + 8) : 0u;
+        f[k][3] = v1 ? *reinterpret_cast<const uint32_t*>(q1 + 16 * k + 8) : 0u;
+      }
+    };
+    uint32_t qf[D / 16][4];
+    if (w0 < w1) load_q(p, qf);
     for (long long w = w0; w < w1;) {
       const int n = (int)min((long long)(p.nb - p.blk), w1 - w);
       const int kvh = p.h / a.row_blocks, rb = p.h - kvh * a.row_blocks;
@@ -237,19 +297,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const int head0 = kvh * a.group + 16 * rb;
       const int kv = min(a.b.kv_len[p.b], cap);
       if (threadIdx.x == 0 && a.b.kv_len[p.b] > cap) note_bad_page();
-      uint32_t qf[D / 16][4];
-      {
-        const __nv_bfloat16* q0 = a.q + p.b * a.ldq + (long long)(head0 + quad) * D + qc;
-        const __nv_bfloat16* q1 = q0 + 8 * D;
-        const bool v0 = quad < nrows, v1 = quad + 8 < nrows;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          qf[k][0] = v0 ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k) : 0u;
-          qf[k][1] = v1 ? *reinterpret_cast<const uint32_t*>(q1 + 16 * k) : 0u;
-          qf[k][2] = v0 ? *reinterpret_cast<const uint32_t*>(q0 + 16 * k + 8) : 0u;
-          qf[k][3] = v1 ? *reinterpret_cast<const uint32_t*>(q1 + 16 * k + 8) : 0u;
-        }
-      }
       float o[D / 8][4] = {};
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // rows quad and quad + 8
       for (int i = 0; i < n; ++i, ++it) {
@@ -262,12 +309,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (key0 < kv) {
           float s[2][4] = {};
           {
-            const int r = kq + ((lane >> 4) << 3) + (lane & 7), cb = (lane >> 3) & 1;
+            const int r = in_box + ((lane >> 4) << 3) + (lane & 7), cb = (lane >> 3) & 1;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               uint32_t f[4];
               const int ch = (k & 3) * 2 + cb;
-              ldsm_x4(kb + (k >> 2) * (kBlockKeys * 128) + r * 128 + ((ch ^ (r & 7)) << 4), f);
+              ldsm_x4(kb + box_at + (k >> 2) * half_at + r * 128 + ((ch ^ (r & 7)) << 4), f);
               mma_bf16(s[0], qf[k], f[0], f[1]);
               mma_bf16(s[1], qf[k], f[2], f[3]);
             }
@@ -324,12 +371,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           l1 += (e[0][2] + e[0][3]) + (e[1][2] + e[1][3]);
           const uint32_t pf[4] = {pack_bf16(e[0][0], e[0][1]), pack_bf16(e[0][2], e[0][3]),
                                   pack_bf16(e[1][0], e[1][1]), pack_bf16(e[1][2], e[1][3])};
-          const int r = kq + (((lane >> 3) & 1) << 3) + (lane & 7), cb = lane >> 4;
+          const int r = in_box + (((lane >> 3) & 1) << 3) + (lane & 7), cb = lane >> 4;
 #pragma unroll
           for (int t = 0; t < D / 16; ++t) {
             uint32_t f[4];
             const int ch = (t & 3) * 2 + cb;
-            ldsm_x4_t(vb + (t >> 2) * (kBlockKeys * 128) + r * 128 + ((ch ^ (r & 7)) << 4), f);
+            ldsm_x4_t(vb + box_at + (t >> 2) * half_at + r * 128 + ((ch ^ (r & 7)) << 4), f);
             if (partial) {  // values that do not exist may be NaN
               f[0] &= vm0;
               f[1] &= vm1;
@@ -343,6 +390,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);
       }
+      DecPos nx = p;  // the next segment, whose queries load during the join
+      nx.blk = p.blk + n;
+      if (nx.blk == nx.nb) dec_next_pair(a, nx, heads);
+      if (w + n < w1) load_q(nx, qf);
       // ------------------------------------------------- join the eight warps
 #pragma unroll
       for (int d = 1; d < 4; d <<= 1) {
@@ -352,8 +403,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       if ((lane & 3) == 0) {
         st_m[warp * 16 + quad] = m0;
         st_m[warp * 16 + quad + 8] = m1;
-        st_l[warp * 16 + quad] = l0;
-        st_l[warp * 16 + quad + 8] = l1;
       }
       auto sync = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
       sync();
@@ -364,33 +413,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         M1 = fmaxf(M1, st_m[v * 16 + quad + 8]);
       }
       const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M1);
-      auto slice = [&](int v, int row, int col) { return merge + (v * 16 + row) * D + ((col + 8 * row) & (D - 1)); };
-      const int v4 = warp & 3;
-      if (wg == 1) {
-#pragma unroll
-        for (int t = 0; t < D / 8; ++t) {
-          if (quad < nrows)
-            *reinterpret_cast<float2*>(slice(v4, quad, 8 * t + qc)) = make_float2(o[t][0] * f0, o[t][1] * f0);
-          if (quad + 8 < nrows)
-            *reinterpret_cast<float2*>(slice(v4, quad + 8, 8 * t + qc)) =
-                make_float2(o[t][2] * f1, o[t][3] * f1);
-        }
+      if ((lane & 3) == 0) {
+        st_l[warp * 16 + quad] = l0 * f0;
+        st_l[warp * 16 + quad + 8] = l1 * f1;
       }
-      sync();
-      if (wg == 0) {
-#pragma unroll
-        for (int t = 0; t < D / 8; ++t) {
-          if (quad < nrows) {
-            float2* at = reinterpret_cast<float2*>(slice(v4, quad, 8 * t + qc));
-            *at = make_float2(at->x + o[t][0] * f0, at->y + o[t][1] * f0);
-          }
-          if (quad + 8 < nrows) {
-            float2* at = reinterpret_cast<float2*>(slice(v4, quad + 8, 8 * t + qc));
-            *at = make_float2(at->x + o[t][2] * f1, at->y + o[t][3] * f1);
-          }
-        }
-      }
-      sync();
       // where the segment goes: whole pairs to O, or (with a prefix to join) to
       // the pair's slot; a partial first segment to slot 2c, a partial last one
       // to 2c + 1
@@ -399,43 +425,61 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                              : !ends ? 2 * (long long)blockIdx.x + 1
                                      : 2 * (long long)a.shares + (long long)p.b * heads + p.h;
       const bool final = starts && ends && a.prefix == 0;
-      for (int e = threadIdx.x; e < nrows * (D / 4); e += 256) {
-        const int row = e / (D / 4), c4 = (e - row * (D / 4)) * 4;
-        float mm = -INFINITY, z = 0.f;
+      // each warp's share of O goes through shared memory, all columns of up to
+      // 8 rows at once or half of them for up to 16: [warp][row][column], rows
+      // turned by 8 columns each
+      auto join = [&](auto rows_tag) {
+        constexpr int NR = decltype(rows_tag)::value, NC = 8 * D / NR;
+        auto place = [&](int v, int row, int col) { return merge + (v * NR + row) * NC + ((col + 8 * row) & (NC - 1)); };
 #pragma unroll
-        for (int v = 0; v < 8; ++v) mm = fmaxf(mm, st_m[v * 16 + row]);
+        for (int c0 = 0; c0 < D; c0 += NC) {
 #pragma unroll
-        for (int v = 0; v < 8; ++v) {
-          const float mv = st_m[v * 16 + row];
-          if (mv != -INFINITY) z += st_l[v * 16 + row] * ex2(mv - mm);
-        }
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int t = 0; t < NC / 8; ++t) {
+            const float(&x)[4] = o[c0 / 8 + t];
+            if (quad < nrows) *reinterpret_cast<float2*>(place(warp, quad, 8 * t + qc)) = make_float2(x[0] * f0, x[1] * f0);
+            if (NR == 16 && quad + 8 < nrows)
+              *reinterpret_cast<float2*>(place(warp, quad + 8, 8 * t + qc)) = make_float2(x[2] * f1, x[3] * f1);
+          }
+          sync();
+          for (int e = threadIdx.x; e < nrows * (NC / 4); e += 256) {
+            const int row = e / (NC / 4), c4 = (e % (NC / 4)) * 4;
+            float z = 0.f;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float4 y = *reinterpret_cast<const float4*>(slice(v, row, c4));
-          x.x += y.x;
-          x.y += y.y;
-          x.z += y.z;
-          x.w += y.w;
+            for (int v = 0; v < 8; ++v) {
+              const float4 y = *reinterpret_cast<const float4*>(place(v, row, c4));
+              z += st_l[v * 16 + row];
+              x.x += y.x;
+              x.y += y.y;
+              x.z += y.z;
+              x.w += y.w;
+            }
+            const float inv = z > 0.f ? 1.f / z : 0.f;
+            x.x *= inv;
+            x.y *= inv;
+            x.z *= inv;
+            x.w *= inv;
+            if (!ok) continue;
+            if (final) {
+              *reinterpret_cast<uint2*>(a.o + p.b * a.ldo + (long long)(head0 + row) * D + c0 + c4) =
+                  make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+            } else {
+              *reinterpret_cast<float4*>(a.so + (slot * a.rows + row) * D + c0 + c4) = x;
+              if (c0 + c4 == 0) {
+                float mm = -INFINITY;
+#pragma unroll
+                for (int v = 0; v < 8; ++v) mm = fmaxf(mm, st_m[v * 16 + row]);
+                a.slse[slot * a.rows + row] = z > 0.f ? mm + log2f(z) : -INFINITY;
+              }
+            }
+          }
+          sync();  // the buffer may be written again
         }
-        const float inv = z > 0.f ? 1.f / z : 0.f;
-        x.x *= inv;
-        x.y *= inv;
-        x.z *= inv;
-        x.w *= inv;
-        if (!ok) continue;
-        if (final) {
-          *reinterpret_cast<uint2*>(a.o + p.b * a.ldo + (long long)(head0 + row) * D + c4) =
-              make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
-        } else {
-          *reinterpret_cast<float4*>(a.so + (slot * a.rows + row) * D + c4) = x;
-          if (c4 == 0) a.slse[slot * a.rows + row] = z > 0.f ? mm + log2f(z) : -INFINITY;
-        }
-      }
-      sync();  // the buffers may be written again
+      };
+      if (nrows <= 8) join(std::integral_constant<int, 8>{});
+      else join(std::integral_constant<int, 16>{});
       w += n;
-      p.blk += n - 1;
-      if (++p.blk == p.nb) dec_next_pair(a, p, heads);
+      p = nx;
     }
   }
   if (a.prefix != 0) grid_dep_wait();  // k_join waits for this grid only
@@ -462,18 +506,24 @@ __global__ void __launch_bounds__(128) k_join(const DecArgs a) {
   // the lengths are inputs of the call: k_decode_attn lets this grid start
   // only after its own wait, so they are complete here
   const int heads = a.c_.n_kv_heads * a.row_blocks;
-  long long before, total;
-  dec_sums(a, b, lane, before, total);
-  total *= heads;
+  long long before = 0, total = 0;
+  for (int i = lane; i < a.b.batch; i += 32) {
+    const int n = dec_blocks(a, i);
+    total += n;
+    if (i < b) before += n;
+  }
+  before = warp_sum(before, a.b.batch <= 32);
+  total = warp_sum(total, a.b.batch <= 32) * heads;
   const int kvh = h / a.group, hr = h - kvh * a.group;
   const int hb = kvh * a.row_blocks + hr / 16, row = hr & 15;
   const int nb = dec_blocks(a, b);
   const long long s0 = before * heads + (long long)hb * nb, s1 = s0 + nb;
   // shares that hold the pair's first and last block
+  const Shares shares(total, a.shares);
   int c0 = 0, c1 = -1;
   if (nb > 0) {
-    c0 = (int)(((s0 + 1) * a.shares - 1) / total);  // largest c with floor(total c / shares) <= s0
-    c1 = (int)((s1 * a.shares - 1) / total);
+    c0 = shares.of(s0);
+    c1 = shares.of(s1 - 1);
   }
   // the prefix's parts, as ShareWalk lays them out: pairs of `keys` keys each
   int p0 = 0, np = 0, item = 0, prow = 0;
@@ -510,14 +560,11 @@ __global__ void __launch_bounds__(128) k_join(const DecArgs a) {
         src = a.po + (slot * 256 + prow) * D;
       }
     } else if (i < n) {
-      const long long c = c0 + i - np, w0 = total * c / a.shares, w1 = total * (c + 1) / a.shares;
-      if (w0 < w1) {  // else: fewer blocks than shares
-        const long long slot = w0 > s0   ? 2 * c
-                               : w1 < s1 ? 2 * c + 1
-                                         : 2ll * a.shares + (long long)b * heads + hb;
-        lse = a.slse[slot * a.rows + row];
-        src = a.so + (slot * a.rows + row) * D;
-      }
+      const long long c = c0 + i - np, slot = shares.start(c) > s0       ? 2 * c
+                                              : shares.start(c + 1) < s1 ? 2 * c + 1
+                                                                         : 2ll * a.shares + (long long)b * heads + hb;
+      lse = a.slse[slot * a.rows + row];
+      src = a.so + (slot * a.rows + row) * D;
     }
     return lse;
   };

@@ -113,6 +113,23 @@ bool make_map_bf16_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 rows of `inner` = 64 or 128 elements, [slices][rows][inner] with strides
+// in bytes, as a 4-D tensor (64 elements, rows, inner / 64, slices): one copy
+// brings a box of whole rows, its 64-element column groups one behind the other
+// in shared memory, each in the 128-byte swizzle.
+bool make_map_bf16_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t slices,
+                        uint64_t row_stride, uint64_t slice_stride, uint32_t box_rows, uint32_t box_slices) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {64, rows, inner / 64, slices};
+  cuuint64_t strides[3] = {row_stride, 128, slice_stride};
+  cuuint32_t box[4] = {64, box_rows, (cuuint32_t)(inner / 64), box_slices};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
@@ -1771,7 +1788,7 @@ struct serq_kv_cache {
   int n_pages, page_size, page_shift, n_kv_heads, head_dim, device;
   int64_t page_stride;
   __nv_bfloat16 *K, *V;
-  CUtensorMap tm[2][2];  // K, V; box: 64 elements x min(page_size, 128 | 64) slots of one head
+  CUtensorMap tm[2][2];  // K, V; prompt tiles: 64 elements x min(page_size, 128) slots; decode: whole rows x min(page_size, 64)
 };
 
 namespace {
@@ -1936,13 +1953,14 @@ serq_status serq_kv_cache_create(void* K, void* V, int n_pages, int page_size, i
   c->K = static_cast<__nv_bfloat16*>(K);
   c->V = static_cast<__nv_bfloat16*>(V);
   cudaGetDevice(&c->device);
-  for (int i = 0; i < 4; ++i)
-    if (!make_map_bf16_3d(&c->tm[i & 1][i >> 1], i & 1 ? V : K, head_dim, (uint64_t)n_kv_heads * page_size, n_pages,
-                          (uint64_t)head_dim * 2, (uint64_t)page_stride * 2, std::min(page_size, i < 2 ? 128 : 64),
-                          1)) {
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t rows = (uint64_t)n_kv_heads * page_size, row = (uint64_t)head_dim * 2, slice = (uint64_t)page_stride * 2;
+    if (!make_map_bf16_3d(&c->tm[i][0], i ? V : K, head_dim, rows, n_pages, row, slice, std::min(page_size, 128), 1) ||
+        !make_map_bf16_rows(&c->tm[i][1], i ? V : K, head_dim, rows, n_pages, row, slice, std::min(page_size, 64), 1)) {
       delete c;
       return fail(SERQ_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
     }
+  }
   *out = c;
   return ok();
 }
