@@ -10,6 +10,9 @@ it through the fused two-accumulator GEMM (q/k/v/o 4096x4096, gate/up
 Other workloads (--workload): llama2_7b_decode (M tokens, default 16, CUDA
 graphs, HBM roofline), llama3_8b_w4a8 (M = 4096, INT8 activations),
 mlp_block (gate/up -> SiLU*mul + quantize -> down, M = 4096).
+With --attention a layer workload also runs its attention half between q/k/v
+and o_proj (rotation and cache append, prompt or decode attention, o_proj's
+flatten/permute); the TOPS stay those of the linears.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl serq|reference]
 
@@ -60,9 +63,17 @@ def parse():
                     help="override the workload's quantization mode (same shapes)")
     ap.add_argument("--no-group", action="store_true",
                     help="one launch per projection instead of one per shared-input group")
+    ap.add_argument("--attention", action="store_true",
+                    help="layer workloads: run the attention half between q/k/v and o_proj in the step")
+    ap.add_argument("--context", type=int, default=2048,
+                    help="--attention, decode: cached tokens per sequence")
     ap.add_argument("--profile", action="store_true",
                     help="short run for a profiler: no e2e, no CPU baseline")
     a = ap.parse_args()
+    if a.attention and a.workload in ("mlp_block", "l2qer_compare"):
+        ap.error("--attention goes with the layer workloads")
+    if a.context < 0:
+        ap.error("--context must not be negative")
     if a.M is None:
         a.M = {"llama2_7b_prefill": 2048, "llama2_7b_decode": 16, "llama3_8b_w4a8": 4096,
                "mlp_block": 4096, "l2qer_compare": 2048}[a.workload]
@@ -230,6 +241,42 @@ class ClockSampler:
 # --------------------------------------------------------------------------
 # GPU workloads
 # --------------------------------------------------------------------------
+class AttentionHalf:
+    """What stands between q/k/v and o_proj: one prompt of M tokens, or in
+    decode M sequences of `context` cached tokens and one new one each; heads
+    of 128, the synthetic projections' outputs as queries, keys and values."""
+
+    HEAD, PAGE = 128, 64
+
+    def __init__(self, S, torch, dev, n_q, n_kv, M, decode, context):
+        self.S, self.decode = S, decode
+        i32 = lambda a: torch.as_tensor(a, dtype=torch.int32, device=dev)
+        lens = [context + 1] * M if decode else [M]
+        pages = -(-lens[0] // self.PAGE)
+        self.rope = S.Rope(self.HEAD)
+        self.cache = S.KVCache(pages * len(lens), self.PAGE, n_kv // self.HEAD, self.HEAD, device=dev)
+        self.cache.K.normal_()
+        self.cache.V.normal_()
+        self.cu_q = i32(list(range(M + 1)) if decode else [0, M])
+        self.kv_len = i32(lens)
+        self.table = torch.arange(pages * len(lens), dtype=torch.int32, device=dev).view(len(lens), pages)
+        self.Q = torch.empty((M, n_q), dtype=torch.bfloat16, device=dev)
+        self.O = torch.empty_like(self.Q)
+        heads = n_q // self.HEAD
+        self.ws = (S.attn_decode_ws(self.cache, M, heads, pages) if decode else
+                   S.attn_prefill_ws(self.cache, M, heads, 1, pages))
+        self.launches = 4 if decode or self.ws is not None else 3
+
+    def run(self, q, k, v, o_layer, out, stream):
+        S = self.S
+        S.rope_append(self.rope, self.cache, q, k, v, self.cu_q, self.kv_len, self.table, Qout=self.Q, stream=stream)
+        if self.decode:
+            S.attn_decode(self.cache, self.Q, self.kv_len, self.table, O=self.O, ws=self.ws, stream=stream)
+        else:
+            S.attn_prefill(self.cache, self.Q, self.cu_q, self.kv_len, self.table, O=self.O, ws=self.ws, stream=stream)
+        S.flatten_permute(o_layer, self.O, Xh=out, stream=stream)
+
+
 class LayerWorkload:
     """Independent projections grouped by shared input (a decoder layer)."""
 
@@ -277,12 +324,24 @@ class LayerWorkload:
         n_gemm_launches = len(self.grp) if self.grouped else len(self.gemms)
         n_quant = sum(0 if self.fused(i, ps) else 1 for i, ps in self.grp)
         self.launches_per_step = n_quant + n_gemm_launches
+        self.attn = None
+        if args.attention:
+            width = {n: N for n, _, N in self.gemms}
+            self.attn = AttentionHalf(S, torch, dev, width["q_proj"], width["k_proj"], M, self.decode, args.context)
+            self.launches_per_step += self.attn.launches
         self.weight_mb = sum(p.W.size for p in wl.projections) / 2 / 1e6
 
     def describe(self):
         shapes = ", ".join(f"{n} {K}x{N}" for n, K, N in self.gemms)
         return (f"{self.name}_{self.mode}_r{self.r}: one decoder layer's {len(self.gemms)} projections "
-                f"({shapes}), {len(self.grp)} shared-input quantizes, M = {self.M} tokens per GPU")
+                f"({shapes}), {len(self.grp)} shared-input quantizes, M = {self.M} tokens per GPU"
+                + (", attention half included" if self.attn else ""))
+
+    def attention(self, c, a, iname, stream):
+        """The attention half, in front of the group that reads its output."""
+        if self.attn and iname == "o_in":
+            self.attn.run(self.Y["q_proj"], self.Y["k_proj"], self.Y["v_proj"], self.layers[c]["o_proj"],
+                          self.flat[iname][a], stream)
 
     def fused(self, iname, projs):
         return fuses_act_quantize(self.decode, self.grouped, self.M, self.wl.inputs[iname].K)
@@ -291,6 +350,8 @@ class LayerWorkload:
         S, torch = self.S, self.torch
         c, a = i % N_WEIGHT_COPIES, i % N_ACT_COPIES
         for iname, projs in self.grp:
+            if not gemm_only:
+                self.attention(c, a, iname, stream)
             if self.fused(iname, projs):
                 # one launch, quantize included (also in the GEMM-only graph:
                 # it is the GEMV launch of this group)
@@ -329,13 +390,13 @@ class LayerWorkload:
     # step's copies overlap its neighbours' compute
     def host_buffers(self):
         torch = self.torch
-        self.host_in = {i: self.flat[i][0].cpu().pin_memory() for i, _ in self.grp}
+        self.host_in = {i: self.flat[i][0].cpu().pin_memory() for i, _ in self.grp if not (self.attn and i == "o_in")}
         self.host_out = {n: torch.empty(y.shape, dtype=y.dtype).pin_memory() for n, y in self.Y.items()}
         self.Ybuf = [self.Y, {n: torch.empty_like(y) for n, y in self.Y.items()}]
         return self.host_in, self.host_out
 
     def e2e_inputs(self, b):
-        return [(self.host_in[i], self.flat[i][b]) for i, _ in self.grp]
+        return [(self.host_in[i], self.flat[i][b]) for i, _ in self.grp if i in self.host_in]
 
     def e2e_outputs(self, b):
         return [(self.Ybuf[b][n], self.host_out[n]) for n in self.Y]
@@ -347,6 +408,7 @@ class LayerWorkload:
         self.Y = self.Ybuf[b]
         try:
             for iname, projs in self.grp:
+                self.attention(c, b, iname, stream)
                 if self.fused(iname, projs):
                     S.linear_group_act([self.layers[c][p.name] for p in projs], self.flat[iname][b],
                                        Ys=[self.Y[p.name] for p in projs], Xq=self.Xq[iname], sx=self.sx[iname],

@@ -514,3 +514,137 @@ def test_refusals(S):
               lambda: S.KVCache(K=cache.K)):
         with pytest.raises(ValueError):
             f()
+
+
+# ------------------------------------------------------------ harder batches
+def test_many_sequences(S):
+    """More sequences than a warp has lanes, some empty; every kind of split."""
+    rng = np.random.default_rng(51)
+    Hq, Hkv, D, page = 4, 2, 64, 16
+    q_lens = [int(n) for n in rng.choice([0, 1, 2, 40, 70], size=71)]
+    kv_lens = [n + int(rng.integers(0, 90)) if n or rng.random() < 0.5 else 0 for n in q_lens]
+    cu = np.concatenate([[0], np.cumsum(q_lens)])
+    T = int(cu[-1])
+    table, n_pages = make_table(rng, kv_lens, page)
+    cache, k, v = make_cache(S, rng, kv_lens, table, n_pages, Hkv, page, D)
+    q = bf(rng.normal(size=(T, Hq * D)))
+    o = S.attn_prefill(cache, q.cuda(), i32(cu), i32(kv_lens), i32(table))
+    ref, tol, written = A.attention(f64(q).reshape(T, Hq, D), k, v, cu, kv_lens, table)
+    check(o, ref, tol, written, Hq, D)
+    B = len(kv_lens)
+    q = bf(rng.normal(size=(B, Hq * D)))
+    o = S.attn_decode(cache, q.cuda(), i32(kv_lens), i32(table))
+    ref, tol, written = A.attention(f64(q).reshape(B, Hq, D), k, v, range(B + 1), kv_lens, table)
+    check(o, ref, tol, written, Hq, D)
+    assert S.device_error() == 0
+
+
+@pytest.mark.parametrize("q_lens,past,Hq,Hkv,D,page", [
+    ([300, 5, 0, 90], [2000, 1500, 9, 0], 2, 1, 128, 64),   # few tile pairs: shares that cut items, one head
+    ([100], [3000], 8, 2, 64, 128),
+    ([17, 33], [4000, 10], 14, 2, 128, 16),
+    ([130], [1000], 2, 2, 128, 256),
+])
+def test_prefill_shares(S, q_lens, past, Hq, Hkv, D, page):
+    """Work cut into equal shares; the workspace holds NaN before the call."""
+    rng = np.random.default_rng(sum(q_lens) + D)
+    kv_lens = [a + b for a, b in zip(q_lens, past)]
+    cu = np.concatenate([[0], np.cumsum(q_lens)])
+    T = int(cu[-1])
+    table, n_pages = make_table(rng, kv_lens, page)
+    cache, k, v = make_cache(S, rng, kv_lens, table, n_pages, Hkv, page, D)
+    q = bf(rng.normal(size=(T, Hq * D)) * 1.5)
+    ws = S.attn_prefill_ws(cache, T, Hq, len(kv_lens), table.shape[1])
+    assert ws is not None
+    ws.view(torch.float32).fill_(float("nan"))
+    o = S.attn_prefill(cache, q.cuda(), i32(cu), i32(kv_lens), i32(table), ws=ws)
+    ref, tol, written = A.attention(f64(q).reshape(T, Hq, D), k, v, cu, kv_lens, table)
+    check(o, ref, tol, written, Hq, D)
+    with pytest.raises(S.SerqError) as e:
+        S.attn_prefill(cache, q.cuda(), i32(cu), i32(kv_lens), i32(table), ws=ws[:-16])
+    assert e.value.status == S.ERR_INVALID_ARG and "workspace" in str(e.value)
+    assert S.device_error() == 0
+
+
+def test_decode_workspace_is_written_before_it_is_read(S):
+    rng = np.random.default_rng(53)
+    kv_lens, prefix, Hq, Hkv, D, page = [1024 + n for n in (0, 1, 700, 64, 5)], 1024, 8, 2, 128, 64
+    table, n_pages = make_table(rng, kv_lens, page, shared=prefix // page)
+    cache, k, v = make_cache(S, rng, kv_lens, table, n_pages, Hkv, page, D)
+    q = bf(rng.normal(size=(5, Hq * D)))
+    ref, tol, written = A.attention(f64(q).reshape(5, Hq, D), k, v, range(6), kv_lens, table)
+    for p in (0, prefix):
+        ws = S.attn_decode_ws(cache, 5, Hq, table.shape[1], p)
+        for fill in (float("nan"), 1e30):
+            ws.view(torch.float32).fill_(fill)
+            o = S.attn_decode(cache, q.cuda(), i32(kv_lens), i32(table), prefix_len=p, ws=ws)
+            check(o, ref, tol, written, Hq, D)
+
+
+def test_two_streams_with_a_workspace_each(S):
+    rng = np.random.default_rng(54)
+    Hq, Hkv, D, page = 8, 2, 128, 64
+    jobs = []
+    for kv in ([3000, 10], [77, 2048]):
+        table, n_pages = make_table(rng, kv, page)
+        cache, k, v = make_cache(S, rng, kv, table, n_pages, Hkv, page, D)
+        q = bf(rng.normal(size=(2, Hq * D)))
+        ref = A.attention(f64(q).reshape(2, Hq, D), k, v, range(3), kv, table)
+        jobs.append((cache, q.cuda(), i32(kv), i32(table), S.attn_decode_ws(cache, 2, Hq, table.shape[1]), ref,
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for i, (cache, q, kv, tab, ws, ref, st) in enumerate(jobs):
+            with torch.cuda.stream(st):
+                outs[i].append(S.attn_decode(cache, q, kv, tab, ws=ws))
+                outs[i].append(S.attn_prefill(cache, q, i32([0, 1, 2]), kv, tab))
+    torch.cuda.synchronize()
+    for (cache, q, kv, tab, ws, (r, tol, written), st), os_ in zip(jobs, outs):
+        for o in os_:
+            check(o, r, tol, written, Hq, D)
+
+
+def test_offsets_beyond_32_bits(S):
+    """Pages far apart: element offsets of the cache pass 2^31."""
+    rng = np.random.default_rng(55)
+    Hq, Hkv, D, page, stride, n_pages = 4, 2, 128, 64, 1 << 29, 6
+    raw = [torch.empty((n_pages - 1) * stride + Hkv * page * D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    K, V = (t.as_strided((n_pages, Hkv, page, D), (stride, page * D, D, 1)) for t in raw)
+    K.fill_(float("nan")), V.fill_(float("nan"))
+    cache = S.KVCache(K=K, V=V)
+    kv, table = [6 * page - 3], np.array([[5, 0, 4, 2, 3, 1]])
+    T = kv[0]
+    q, k, v = (bf(rng.normal(size=(T, h * D))) for h in (Hq, Hkv, Hkv))
+    out = S.rope_append(S.Rope(D), cache, q.cuda(), k.cuda(), v.cuda(), i32([0, T]), i32(kv), i32(table))
+    o = S.attn_prefill(cache, out, i32([0, T]), i32(kv), i32(table))
+    od = S.attn_decode(cache, out[-1:], i32(kv), i32(table))
+    yk, mag = A.rotate(f64(k).reshape(T, Hkv, D), np.arange(T), A.frequencies(D))
+    ck, cv = f64(cache.K), f64(cache.V)
+    for t in range(T):
+        assert np.all(np.abs(ck[table[0, t // page], :, t % page] - yk[t]) <= A.rotate_bound(yk[t], mag[t], False))
+    ref, tol, written = A.attention(f64(out).reshape(T, Hq, D), np.nan_to_num(ck), np.nan_to_num(cv), [0, T], kv, table)
+    check(o, ref, tol, written, Hq, D)
+    check(od, ref[-1:], tol[-1:], written[-1:], Hq, D)
+    assert S.device_error() == 0
+
+
+def test_infinite_and_nan_outside_the_batch(S):
+    """Rows of Q outside the batch and cache slots behind the sequences hold
+    NaN and infinities; results do not see them."""
+    rng = np.random.default_rng(56)
+    Hq, Hkv, D, page = 4, 4, 128, 32
+    q_lens, kv_lens = [50, 3], [170, 35]
+    cu = np.concatenate([[0], np.cumsum(q_lens)]) + 2
+    T = int(cu[-1]) + 80
+    table, n_pages = make_table(rng, kv_lens, page)
+    cache, k, v = make_cache(S, rng, kv_lens, table, n_pages, Hkv, page, D)
+    cache.V[torch.isnan(cache.V)] = float("inf")
+    cache.K[torch.isnan(cache.K)] = float("-inf")
+    q = bf(rng.normal(size=(T, Hq * D)))
+    qd = q.cuda()
+    qd[:2], qd[int(cu[-1]):] = float("nan"), float("inf")
+    o = torch.full_like(qd, 5.0)
+    S.attn_prefill(cache, qd, i32(cu), i32(kv_lens), i32(table), O=o)
+    ref, tol, written = A.attention(f64(q).reshape(T, Hq, D), k, v, cu, kv_lens, table)
+    check(o, ref, tol, written, Hq, D, fill=5.0)
