@@ -74,24 +74,6 @@ __device__ __forceinline__ long long warp_sum(long long v, bool small) {
   return v;
 }
 
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
-// Equal shares of `total` blocks: the first total % G have one block more.
-struct Shares {
-  long long base, more;  // blocks of a share, shares with one more
-  __device__ Shares(long long total, int g) {
-    base = quotient(total, g);
-    more = total - base * g;
-  }
-  __device__ long long start(long long c) const { return c * base + min(c, more); }
-  __device__ int of(long long w) const {  // the share that holds block w
-    const long long m = more * (base + 1);
-    return (int)(w < m ? quotient(w, base + 1) : more + quotient(w - m, base));
-  }
-};
-
 // Position in the batch's run of blocks.
 struct DecPos {
   int b, h, blk, nb;  // sequence, head block, next block, blocks of the sequence
@@ -537,53 +519,57 @@ __global__ void __launch_bounds__(128) k_join(const DecArgs a) {
   }
   // the prefix's parts, as ShareWalk lays them out: pairs of `keys` keys each
   int p0 = 0, np = 0, item = 0, prow = 0;
-  long long pstart = 0, ptotal = 1, keys = 0;
+  long long pstart = 0, keys = 0, ptotal = 0;
   if (a.prefix) {
     int k = 0;
     for (int i = lane; i < a.b.batch; i += 32) k = max(k, min(a.b.kv_len[i], a.prefix));
     keys = __reduce_max_sync(0xffffffffu, k);
-    if (keys > 0) {
-      const int pair = 2 * a.ptokens, pairs = ceil_div(a.b.batch, pair), tile = b / pair;
-      const int in = b - tile * pair, x = in >= a.ptokens;
-      prow = 128 * x + (in - x * a.ptokens) * a.group + hr;
-      item = kvh * pairs + tile;
-      pstart = item * keys;
-      ptotal = keys * pairs * a.c_.n_kv_heads;
-      p0 = (int)(((pstart + 1) * a.pshares - 1) / ptotal);
-      np = (int)(((pstart + keys) * a.pshares - 1) / ptotal) - p0 + 1;
-    }
+    const int pair = 2 * a.ptokens, pairs = ceil_div(a.b.batch, pair), tile = b / pair;
+    const int in = b - tile * pair, x = in >= a.ptokens;
+    prow = 128 * x + (in - x * a.ptokens) * a.group + hr;
+    item = kvh * pairs + tile;
+    pstart = item * keys;
+    ptotal = keys * pairs * a.c_.n_kv_heads;
   }
-  grid_dep_wait();
-  if (nb > 0 && c0 == c1 && a.prefix == 0) return;  // finished by its CTA
+  const Shares pshares(ptotal, max(a.pshares, 1));
+  if (keys > 0) {
+    p0 = pshares.of(pstart);
+    np = pshares.of(pstart + keys - 1) - p0 + 1;
+  }
   const int n = np + c1 - c0 + 1;
-  // part i: log-sum and place of its row (in rows of D floats)
-  auto find = [&](int i, const float*& src) {
-    float lse = -INFINITY;
+  // Place of part i: its row (in rows of D floats) and log-sum, null when it
+  // has none.
+  auto place = [&](int i, const float*& src, const float*& lse) {
+    src = a.so;
+    lse = nullptr;
     if (i < np) {
       const long long c = p0 + i;
-      const long long lo = max(0ll, ptotal * c / a.pshares - pstart), hi = min(keys, ptotal * (c + 1) / a.pshares - pstart);
+      const long long lo = max(0ll, pshares.start(c) - pstart), hi = min(keys, pshares.start(c + 1) - pstart);
       const int steps = ceil_div((int)keys, kTileKeys);
       const int shi = hi == keys ? steps : (int)(hi / kTileKeys);
       if (lo < hi && lo / kTileKeys < shi) {  // else: no step of its own
         const long long slot = lo > 0 ? 2 * c : hi < keys ? 2 * c + 1 : 2ll * a.pshares + item;
-        lse = a.plse[slot * 256 + prow];
+        lse = a.plse + slot * 256 + prow;
         src = a.po + (slot * 256 + prow) * D;
       }
     } else if (i < n) {
       const long long c = c0 + i - np, slot = shares.start(c) > s0       ? 2 * c
                                               : shares.start(c + 1) < s1 ? 2 * c + 1
                                                                          : 2ll * a.shares + (long long)b * heads + hb;
-      lse = a.slse[slot * a.rows + row];
+      lse = a.slse + slot * a.rows + row;
       src = a.so + (slot * a.rows + row) * D;
     }
-    return lse;
   };
+  const float *src, *at_lse;
+  place(lane * W + mine, src, at_lse);
+  grid_dep_wait();
+  if (nb > 0 && c0 == c1 && a.prefix == 0) return;  // finished by its CTA
   constexpr int E = D / 32;
   if ((int)blockIdx.y * (4 / W) + warp / W >= a.n_heads) return;
   float acc[E] = {}, z = 0.f, top = -INFINITY;
   for (int i0 = 0; i0 * W < n; i0 += 32) {
-    const float* src = a.so;
-    const float lse = find((i0 + lane) * W + mine, src);
+    if (i0) place((i0 + lane) * W + mine, src, at_lse);
+    const float lse = at_lse ? *at_lse : -INFINITY;
     float mx = lse;
 #pragma unroll
     for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -598,15 +584,21 @@ __global__ void __launch_bounds__(128) k_join(const DecArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= f;
     const int cnt = min(32, (n - mine + W - 1) / W - i0);
-#pragma unroll 8
-    for (int i = 0; i < cnt; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* from = reinterpret_cast<const float*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
-      if (wi != 0.f) {  // an empty part's row is not written
+    for (int i1 = 0; i1 < cnt; i1 += 8) {
+      // eight rows in flight; an empty part's row is not written, nor read
+      float x[8][E], wi[8];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += wi * from[lane * E + e];
+      for (int i = 0; i < 8; ++i) {
+        wi[i] = __shfl_sync(0xffffffffu, w, (i1 + i) & 31);
+        const float* from = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), (i1 + i) & 31));
+        if (i1 + i >= cnt) wi[i] = 0.f;
+        load_part<E>(from + lane * E, wi[i] != 0.f, x[i]);
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += wi[i] * x[i][e];
     }
   }
   if (W > 1) {

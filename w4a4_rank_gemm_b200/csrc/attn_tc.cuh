@@ -238,10 +238,28 @@ __device__ __forceinline__ void ranked_item(const TcArgs& a, const Pairs& mine, 
   }
 }
 
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// Equal shares of `total` units of work: the first total % G have one more.
+struct Shares {
+  long long base, more;  // of a share, shares with one more
+  __device__ Shares(long long total, int g) {
+    base = quotient(total, g);
+    more = total - base * g;
+  }
+  __device__ long long start(long long c) const { return c * base + min(c, more); }
+  __device__ int of(long long w) const {  // the share that holds unit w
+    const long long m = more * (base + 1);
+    return (int)(w < m ? quotient(w, base + 1) : more + quotient(w - m, base));
+  }
+};
+
 // Equal shares.  Work is laid out by sequence, kv head and tile pair and
 // measured in keys, m_i = past + (i + 1) pair for pair i (every pair of the
-// shared prefix: its keys), whose sums have a closed form; share c of G is
-// [W c / G, W (c + 1) / G).  An item cut at key x is cut at step x / 128.
+// shared prefix: its keys), whose sums have a closed form.  An item cut at key
+// x is cut at step x / 128.
 struct Measure {
   long long past, inc;  // m_i = past + (i + 1) inc
   __device__ long long of(int i) const { return past + (i + 1) * inc; }
@@ -302,13 +320,14 @@ struct ShareWalk {
       share_sums(a, 0, lane, before, total);
     }
     total *= heads;
-    x = total * blockIdx.x / a.shares;
-    x1 = total * (blockIdx.x + 1) / a.shares;
+    const Shares shares(total, a.shares);
+    x = shares.start(blockIdx.x);
+    x1 = shares.start(blockIdx.x + 1);
     if (x >= x1) return;
     seq = 0;
     long long base = 0, per_head = 0;
     if (a.prefix) {
-      per_head = total / heads;
+      per_head = quotient(total, heads);
     } else {
       for (int b0 = 0;; b0 += 32) {
         const Pairs p = load_pairs(a, b0 + lane);
@@ -332,7 +351,7 @@ struct ShareWalk {
       s = load_pairs(a, seq);
     }
     const long long rest = x - base * heads;
-    kvh = (int)(rest / per_head);
+    kvh = (int)quotient(rest, per_head);
     const long long in = rest - kvh * per_head;
     const Measure m = measure(a, s);
     int lo = 0, hi = s.np;  // the tile with before(lo) <= in < before(lo + 1)
@@ -915,6 +934,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
+// E = 2 or 4 consecutive floats, or zeros without a read.  (A branch around
+// the read would make each of a row's parts wait for the one before it.)
+template <int E>
+__device__ __forceinline__ void load_part(const float* p, bool take, float (&x)[E]) {
+  if constexpr (E == 4)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\tmov.f32 %0, 0f00000000;\n\tmov.f32 %1, 0f00000000;\n\t"
+        "mov.f32 %2, 0f00000000;\n\tmov.f32 %3, 0f00000000;\n\t@q ld.global.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+        : "l"(p), "r"((int)take));
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %3, 0;\n\tmov.f32 %0, 0f00000000;\n\tmov.f32 %1, 0f00000000;\n\t"
+        "@q ld.global.v2.f32 {%0, %1}, [%2];\n\t}"
+        : "=f"(x[0]), "=f"(x[1])
+        : "l"(p), "r"((int)take));
+}
+
 // Joins the parts of items that shares cut:
 //   O = sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M),  s in share order.
 // One CTA per tile pair, kv head and 32 rows; 4 rows per warp.
@@ -942,8 +979,12 @@ __global__ void __launch_bounds__(256) k_merge(const TcArgs a) {
     }
     tile -= __shfl_sync(0xffffffffu, incl, 31);
   }
-  grid_dep_wait();
-  if (seq < 0) return;
+  // (Every CTA waits before it leaves: what follows in the stream may rely on
+  // this grid's end for k_attn's.)
+  if (seq < 0) {
+    grid_dep_wait();
+    return;
+  }
   const Pairs s = load_pairs(a, seq);
   long long before, total;
   share_sums(a, seq, lane, before, total);
@@ -951,11 +992,12 @@ __global__ void __launch_bounds__(256) k_merge(const TcArgs a) {
   const long long s0 = before * heads + kvh * m.before(s.np) + m.before(tile), size = m.of(tile);
   total *= heads;
   const int steps = pair_steps(s, tile, pair);
-  const int c0 = (int)(((s0 + 1) * a.shares - 1) / total), c1 = (int)(((s0 + size) * a.shares - 1) / total);
+  const Shares shares(total, a.shares);
+  const int c0 = shares.of(s0), c1 = shares.of(s0 + size - 1);
   // slot of share c's part; -1: no step of the item, -2: all of them
   auto part = [&](int c) {
     if (c > c1) return -1;
-    const long long lo = max(0ll, total * c / a.shares - s0), hi = min(size, total * (c + 1) / a.shares - s0);
+    const long long lo = max(0ll, shares.start(c) - s0), hi = min(size, shares.start(c + 1) - s0);
     if (lo >= hi) return -1;
     const int slo = (int)min((long long)steps, lo / kTileKeys);
     const int shi = hi == size ? steps : (int)min((long long)steps, hi / kTileKeys);
@@ -963,6 +1005,7 @@ __global__ void __launch_bounds__(256) k_merge(const TcArgs a) {
   };
   bool whole = steps == 0;
   for (int c = c0 + lane; c <= c1; c += 32) whole |= part(c) == -2;
+  grid_dep_wait();
   if (__any_sync(0xffffffffu, whole)) return;  // finished by its CTA
   constexpr int E = D / 32;
 #pragma unroll 1
@@ -990,15 +1033,20 @@ __global__ void __launch_bounds__(256) k_merge(const TcArgs a) {
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] *= f;
       const int cnt = min(32, c1 - b0 + 1);
-#pragma unroll 4
-      for (int k = 0; k < cnt; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const int sk = __shfl_sync(0xffffffffu, slot, k);
-        if (wk != 0.f) {  // an empty part's row is not written
-          const float* src = a.po + ((long long)sk * 256 + r) * D + lane * E;
+      for (int k1 = 0; k1 < cnt; k1 += 8) {
+        // eight rows in flight; an empty part's row is not written, nor read
+        float v[8][E], wk[8];
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += wk * src[e];
+        for (int k = 0; k < 8; ++k) {
+          wk[k] = __shfl_sync(0xffffffffu, w, (k1 + k) & 31);
+          const int sk = __shfl_sync(0xffffffffu, slot, (k1 + k) & 31);
+          if (k1 + k >= cnt) wk[k] = 0.f;
+          load_part<E>(a.po + ((long long)sk * 256 + r) * D + lane * E, wk[k] != 0.f, v[k]);
         }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += wk[k] * v[k][e];
       }
     }
     const float inv = z > 0.f ? 1.f / z : 0.f;
