@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const uint32_t kb = smem_u32(ring + slot * 2 * L::kOperand), vb = kb + L::kOperand;
         const int key0 = a.prefix + (p.blk + i) * kBlockKeys + kq;  // first key of this warp
         if (key0 < kv) {
-          float s[2][4] = {};
+          // even and odd 16-column steps apart: two chains of products per 8 keys
+          float s[2][4] = {}, s2[2][4] = {};
           {
             const int r = in_box + ((lane >> 4) << 3) + (lane & 7), cb = (lane >> 3) & 1;
 #pragma unroll
@@ -305,8 +306,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
               uint32_t f[4];
               const int ch = (k & 3) * 2 + cb;
               ldsm_x4(kb + box_at + (k >> 2) * half_at + r * 128 + ((ch ^ (r & 7)) << 4), f);
-              mma_bf16(s[0], qf[k], f[0], f[1]);
-              mma_bf16(s[1], qf[k], f[2], f[3]);
+              mma_bf16(k & 1 ? s2[0] : s[0], qf[k], f[0], f[1]);
+              mma_bf16(k & 1 ? s2[1] : s[1], qf[k], f[2], f[3]);
             }
           }
           const bool partial = key0 + 16 > kv;
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[t][e] *= a.sign;
+            for (int e = 0; e < 4; ++e) s[t][e] = (s[t][e] + s2[t][e]) * a.sign;
           if (partial) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
