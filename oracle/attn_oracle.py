@@ -127,7 +127,9 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, limit: np.ndarray,
         w = np.divide(w, z, out=np.zeros_like(w), where=z > 0)
         o[:, h] = w @ vh
         wv = w @ np.abs(vh)
-        # an fp32 score: D products summed in any order, then scale and log2 e
+        # an fp32 score: D products summed in any order, then scale and log2 e;
+        # the exponential of it: 2^-22 by the hardware's, 2.9e-6 (49 steps) by a
+        # degree-4 polynomial; the sum over the row's keys in any order
         mag = np.where(seen, abs(scale) * (np.abs(qh) @ np.abs(kh).T), 0.0)
         ds = (D + 8) * U32 * np.max(mag, axis=1, initial=0.0)[:, None]
         tol[:, h] = U16 * np.abs(o[:, h]) + wv * (1 + U16) * (U16 + 4 * ds + (limit[:, None].clip(0) + 64) * U32)

@@ -648,3 +648,31 @@ def test_infinite_and_nan_outside_the_batch(S):
     S.attn_prefill(cache, qd, i32(cu), i32(kv_lens), i32(table), O=o)
     ref, tol, written = A.attention(f64(q).reshape(T, Hq, D), k, v, cu, kv_lens, table)
     check(o, ref, tol, written, Hq, D, fill=5.0)
+
+
+@pytest.mark.parametrize("shape", ["rising", "falling", "jumps", "flat_then_cliff"])
+@pytest.mark.parametrize("D,Hq", [(128, 1), (64, 2)])
+def test_long_contexts_whose_scores_move(S, shape, D, Hq):
+    """More than 2048 keys, where most steps do without a look at the maximum:
+    scores that rise and fall by far more than the weights' range allows."""
+    rng = np.random.default_rng(61)
+    page, n, kv = 64, 150, 2700
+    table, n_pages = make_table(rng, [kv], page)
+    cache, k, v = make_cache(S, rng, [kv], table, n_pages, 1, page, D)
+    at = np.arange(kv)
+    grow = {"rising": -300 + 0.23 * at, "falling": 300 - 0.23 * at,
+            "jumps": 45.0 * (at // 300) + rng.normal(size=kv), "flat_then_cliff": np.where(at < 2400, 0.0, 500.0)}[shape]
+    for j in range(kv):
+        k[table[0, j // page], 0, j % page] = 0.0
+        k[table[0, j // page], 0, j % page, 0] = grow[j]
+    kt = bf(k)
+    cache.K.copy_(kt)
+    k = f64(kt)
+    q = np.zeros((n, Hq, D), np.float32)
+    q[:, :, 0] = 1.0
+    q[1::3, :, 0] = -1.0  # some rows see the mirror image
+    q[2::3, :, 0] = 0.125
+    cu = [0, n]
+    out = S.attn_prefill(cache, bf(q.reshape(n, -1)).cuda(), i32(cu), i32([kv]), i32(table), scale=1.0)
+    ref, tol, written = A.attention(q.astype(np.float64), k, v, cu, [kv], table, scale=1.0)
+    check(out, ref, tol, written, Hq, D)

@@ -38,6 +38,7 @@ constexpr int kTcThreads = 384;
 constexpr int kRegsIssue = 88, kRegsSoftmax = 208;
 static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= kTcThreads * 168, "register split");
 constexpr int kFmaPairs = 4;  // of 16 pairs of exponentials, how many go to the FMA pipe
+constexpr float kSumLimit = 1.0995116e12f;  // 2^40
 constexpr float kLazyMax = 8.0f;  // log2: how far a row's scores may exceed the maximum in use
 
 struct TcArgs {
@@ -88,14 +89,20 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 2^y for y <= 8 on the FMA pipe: n = round(y), r = y - n in [-1/2, 1/2], a
+// 2^y on the FMA pipe: n = round(y), r = y - n in [-1/2, 1/2], a
 // degree-4 polynomial for 2^r (least maximum relative error with constant term
 // 1, found by reweighted least squares: 2.9e-6, a 1400th of the bf16 rounding that
-// follows), n added to its exponent.  -127 and below give 0.
+// follows), n added to its exponent.  -127 and below give 0; CAP: above 127 as
+// 127, else y stays below that.
+template <bool CAP>
 __device__ __forceinline__ float2 ex2_fma(float2 y) {
   constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: the sum's low bits are n
   y.x = fmaxf(y.x, -127.0f);
   y.y = fmaxf(y.y, -127.0f);
+  if (CAP) {
+    y.x = fminf(y.x, 127.0f);
+    y.y = fminf(y.y, 127.0f);
+  }
   const float2 t = add2(y, make_float2(kRound, kRound));
   const float2 r = add2(y, add2(make_float2(kRound, kRound), make_float2(-t.x, -t.y)));
   float2 p = make_float2(0.009582852944731712f, 0.009582852944731712f);
@@ -401,7 +408,7 @@ struct ShareWalk {
   }
 };
 
-template <int D>
+template <int D, bool LONG>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_attn(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
            const __grid_constant__ CUtensorMap tmV, const TcArgs a) {
@@ -754,6 +761,51 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // weights: held in registers in between, they left too few for the
         // exponentials' temporaries (spills; 750 cycles per 64 keys, not 560).
         const int base = j * kTileKeys;
+        // LONG: past an item's first step the maximum in use mostly still serves,
+        // and then need not be known: weights are formed with it, kept in
+        // registers, and used as long as their sum stays below 2^40 (bf16 and fp32
+        // are as exact there); only a larger sum, a first step and an edge look
+        // for the maximum.  This saves a step's first reading of the scores, at
+        // the price of more code, which short items do not pay back: 300 new
+        // tokens over 300, ten times, 44.7 us with it and 41.5 without, prompts of
+        // 2048 tokens 42.5 and 42.1, of 4096 141 and 147, of 8192 513 and 553.
+        if (LONG && j > it.j0 && base + kTileKeys <= warp_lim) {
+          const float sub = mc == -INFINITY ? 0.f : -mc;
+          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+          uint32_t w[4][16];
+          uint32_t s[2][32];
+          tmem_ld_32x32b_x32(tS, s[0]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld_wait_regs(s[q & 1]);
+            if (q < 3) tmem_ld_32x32b_x32(tS + 32u * (q + 1), s[(q + 1) & 1]);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 s2 = make_float2(__uint_as_float(s[q & 1][2 * e]), __uint_as_float(s[q & 1][2 * e + 1]));
+              const float2 y = fma2(s2, make_float2(a.c, a.c), make_float2(sub, sub));
+              const float2 p = (e * kFmaPairs) % 16 < kFmaPairs ? ex2_fma<true>(y) : make_float2(ex2(y.x), ex2(y.y));
+              if (e & 1) sum1 = add2(sum1, p);
+              else sum0 = add2(sum0, p);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
+              w[q][e] = reinterpret_cast<const uint32_t&>(h);
+            }
+          }
+          const float sum = (sum0.x + sum0.y) + (sum1.x + sum1.y);
+          if (!__any_sync(0xffffffffu, valid && !(sum < kSumLimit))) {
+            l += sum;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              tmem_st_32x32b_x16(tS + 16u * q, w[q]);
+              if (q & 1) {
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q == 1 ? &p_half[x] : &p_full[x]);
+              }
+            }
+            continue;
+          }
+        }
         auto mask = [&](uint32_t(&r)[32], int c0) {  // scores of columns c0 ... c0 + 31
           if (base + c0 + 32 > warp_lim) {
             const int left = lim - base - c0;
@@ -819,7 +871,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const float2 y = fma2(s2, make_float2(a.c, a.c), make_float2(sub, sub));
               // the XU pipe's 16 exponentials a cycle would bound the kernel: part
               // of them is computed on the FMA pipe
-              const float2 p = (e * kFmaPairs) % 16 < kFmaPairs ? ex2_fma(y) : make_float2(ex2(y.x), ex2(y.y));
+              const float2 p = (e * kFmaPairs) % 16 < kFmaPairs ? ex2_fma<false>(y) : make_float2(ex2(y.x), ex2(y.y));
               if (e & 1) sum1 = add2(sum1, p);
               else sum0 = add2(sum0, p);
               const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
@@ -1064,8 +1116,8 @@ inline int tc_shares(long long items, long long keys, int sms) {
 
 template <int D>
 inline cudaError_t launch_tc(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const TcArgs& a,
-                             int ctas, cudaStream_t st) {
-  auto kern = k_attn<D>;
+                             int ctas, bool longer, cudaStream_t st) {
+  auto kern = longer ? k_attn<D, true> : k_attn<D, false>;
   const cudaError_t e = smem_limit(reinterpret_cast<const void*>(kern), TcLayout<D>::kAlloc);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -2058,6 +2058,7 @@ namespace {
 // pack to within 3% of the mean as they are).
 struct PrefillPlan {
   int group, tokens, shares, ctas;
+  bool longer;  // items of more than 16 steps: see k_attn's LONG
   long long pairs;
   size_t ws;
 };
@@ -2070,6 +2071,7 @@ PrefillPlan prefill_plan(const serq_kv_cache* c, int T, int n_heads, int batch, 
   const long long keys = max_kv ? std::min<long long>(max_kv, cap) : cap;
   const bool share = keys > 512 && (items < sms || (items < 2 * sms && keys * batch >= 3ll * T));
   p.shares = share ? serq::attn::tc_shares(items, keys, (int)sms) : 0;
+  p.longer = keys > 2048;
   p.ctas = share ? p.shares : (int)std::min(items, sms);
   p.ws = (size_t)2 * p.shares * 256 * (c->head_dim + 1) * sizeof(float);
   return p;
@@ -2122,8 +2124,8 @@ serq_status serq_attn_prefill(const serq_kv_cache* cache, const void* Q, int ldq
   a.b = {cu_q, kv_len, page_table, batch, max_pages, ld_table};
   a.c_ = cache_args(cache);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = D == 128 ? serq::attn::launch_tc<128>(tmQ, cache->tm[0][0], cache->tm[1][0], a, p.ctas, st)
-                           : serq::attn::launch_tc<64>(tmQ, cache->tm[0][0], cache->tm[1][0], a, p.ctas, st);
+  cudaError_t e = D == 128 ? serq::attn::launch_tc<128>(tmQ, cache->tm[0][0], cache->tm[1][0], a, p.ctas, p.longer, st)
+                           : serq::attn::launch_tc<64>(tmQ, cache->tm[0][0], cache->tm[1][0], a, p.ctas, p.longer, st);
   if (e == cudaSuccess && p.shares)
     e = D == 128 ? serq::attn::launch_merge<128>(a, (int)p.pairs, st) : serq::attn::launch_merge<64>(a, (int)p.pairs, st);
   if (e != cudaSuccess) return cuda_fail(e, "serq_attn_prefill launch");
@@ -2138,6 +2140,7 @@ namespace {
 struct DecodePlan {
   int group, row_blocks, rows, shares;
   int prefix, tokens, pshares;  // the shared prefix's pass, when prefix > 0
+  bool plonger;
   size_t slots, pslots, ws;
 };
 DecodePlan decode_plan(const serq_kv_cache* c, int batch, int n_heads, int max_pages, int prefix_len, int max_kv) {
@@ -2158,6 +2161,7 @@ DecodePlan decode_plan(const serq_kv_cache* c, int batch, int n_heads, int max_p
     p.tokens = serq::attn::kTileRows / p.group;
     const long long items = (long long)(batch + 2 * p.tokens - 1) / (2 * p.tokens) * c->n_kv_heads;
     p.pshares = serq::attn::tc_shares(items, p.prefix, sm_count());
+    p.plonger = items * p.prefix > 2048ll * p.pshares;
     p.pslots = 2 * (size_t)p.pshares + items;
   }
   p.ws = (p.slots * p.rows + p.pslots * 256) * (c->head_dim + 1) * sizeof(float);
@@ -2232,8 +2236,8 @@ serq_status serq_attn_decode(const serq_kv_cache* cache, const void* Q, int ldq,
     a.prefix = p.prefix;
     a.b = d.b;
     a.c_ = d.c_;
-    e = D == 128 ? serq::attn::launch_tc<128>(tmQ, cache->tm[0][0], cache->tm[1][0], a, p.pshares, st)
-                 : serq::attn::launch_tc<64>(tmQ, cache->tm[0][0], cache->tm[1][0], a, p.pshares, st);
+    e = D == 128 ? serq::attn::launch_tc<128>(tmQ, cache->tm[0][0], cache->tm[1][0], a, p.pshares, p.plonger, st)
+                 : serq::attn::launch_tc<64>(tmQ, cache->tm[0][0], cache->tm[1][0], a, p.pshares, p.plonger, st);
   }
   if (e == cudaSuccess)
     e = D == 128 ? serq::attn::launch_decode<128>(cache->tm[0][1], cache->tm[1][1], d, st)
