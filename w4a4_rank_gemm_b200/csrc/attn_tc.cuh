@@ -13,12 +13,12 @@
 // while the tensor core computes one tile's products the other's softmax runs.
 //
 // TMEM (512 columns): S_A, S_B (128 fp32 columns each; P_X in bf16 takes the
-// first 64 columns of S_X once S_X is in registers), O_A, O_B (D each).
+// first 64 columns of S_X as its scores have been read), O_A, O_B (D each).
 //
 // Warps: 0-3 softmax of A (one row per thread), 4-7 of B, 8 loads, 9 MMAs, 10
 // zeroes values behind the last key, 11 decodes work items ahead.
-// Persistent: a CTA takes work items (tile pair, kv head, key split) and the
-// next item's Q, K and first scores overlap the epilogue of the last one.
+// Persistent: a CTA takes work items (tile pair, kv head, range of key steps)
+// and the next item's Q, K and first scores overlap the epilogue of the last.
 #pragma once
 
 #include <algorithm>
@@ -38,8 +38,8 @@ constexpr int kTcThreads = 384;
 constexpr int kRegsIssue = 88, kRegsSoftmax = 208;
 static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= kTcThreads * 168, "register split");
 constexpr int kFmaPairs = 4;  // of 16 pairs of exponentials, how many go to the FMA pipe
-constexpr float kSumLimit = 1.0995116e12f;  // 2^40
-constexpr float kLazyMax = 8.0f;  // log2: how far a row's scores may exceed the maximum in use
+constexpr float kSumLimit = 1.0995116e12f;  // 2^40: see LONG below
+constexpr float kLazyMax = 8.0f;            // log2: how far a row's scores may exceed the maximum in use
 
 struct TcArgs {
   __nv_bfloat16* o;
@@ -470,264 +470,264 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-  if (warp == 8) {
-    // --------------------------------------------------------------- loads
-    if (lane == 0) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-    }
-    const int page = 1 << a.c_.page_shift;
-    const int box = min(page, kTileKeys);         // rows per copy
-    const int copies = kTileKeys / box * L::kHalves;  // per step and operand
-    uint32_t slot = 0, slot_ph = 0, qn[2] = {0, 0};
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&it_full[i & 1], (i >> 1) & 1, abort_flag, kDevTimeoutProducer))) break;
-      const Item it = item_at(i);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&it_empty[i & 1]);
-      if (it.done) break;
-      const int32_t* table = a.b.table + (long long)it.seq * a.b.ldt;
-      const int end = max(it.endA, it.endB);
-      // this lane's copy of a step: its page is looked up one step ahead
-      const int half = lane & (L::kHalves - 1), r = lane / L::kHalves * box;
-      auto lookup = [&](int j) {
-        const int key = j * kTileKeys + r;
-        int pg = a.c_.n_pages;  // past the keys that exist: zeros, from outside the map
-        if (lane < copies && key < it.kv_end) {
-          const int e = table[key >> a.c_.page_shift];
-          if (e >= 0 && e < a.c_.n_pages) pg = e;
-          else note_bad_page();
-        }
-        return pg;
-      };
-      auto load = [&](const CUtensorMap* tm, int j, int pg) {
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait_idle(&kv_empty[slot], slot_ph ^ 1, abort_flag, kDevTimeoutProducer, kWaitLimitNs));
-        if (!ok) return;
-        if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], L::kTile);
-        __syncwarp();
-        if (lane < copies)
-          tma_load_3d(smem + L::oKV + slot * L::kTile + half * (L::kTile / L::kHalves) + r * 128, tm, &kv_full[slot],
-                      64 * half, (it.kvh << a.c_.page_shift) + ((j * kTileKeys + r) & (page - 1)), pg);
-        __syncwarp();
-        if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
-      };
-      int pg = it.j0 < end ? lookup(it.j0) : 0;
-#pragma unroll 1
-      for (int j = it.j0; j < end && ok; ++j) {
-        const int pg_next = j + 1 < end ? lookup(j + 1) : 0;
-        load(&tmK, j, pg);
-        if (j == it.j0) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!ok || (x ? it.endB : it.endA) <= it.j0) continue;
-            ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[x], (qn[x] & 1) ^ 1, abort_flag, kDevTimeoutProducer));
-            if (!ok) continue;
-            ++qn[x];
-            if (lane == 0) {
-              mbar_arrive_expect_tx(&q_full[x], a.tokens * a.group * D * 2);
-              for (int h = 0; h < L::kHalves; ++h)
-                tma_load_3d(smem + L::oQ + x * L::kTile + h * (L::kTile / L::kHalves), &tmQ, &q_full[x], 64 * h,
-                            it.kvh * a.group, it.row0 + x * a.tokens);
-            }
-            __syncwarp();
-          }
-        }
-        if (ok) load(&tmV, j, pg);
-        pg = pg_next;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 8) {
+      // --------------------------------------------------------------- loads
+      if (lane == 0) {
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
       }
-    }
-  } else if (warp == 9) {
-    // ---------------------------------------------------------------- MMAs
-    // One thread runs the whole loop: the tensor core takes a step's 32 MMAs
-    // about as fast as they are issued, so what the issuing thread spends
-    // between them on waits and votes leaves the tensor core idle (with the
-    // whole warp waiting and electing a lane each time, a step of two tiles
-    // took 3400 cycles, 2048 of them MMAs).
-    if (elect_one()) {
-      const uint32_t idesc_qk = umma_idesc_bf16(128, kTileKeys, false, a.neg);
-      constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D, true, false);
-      constexpr int kHalfBytes = L::kTile / L::kHalves;
-      const uint64_t desc_q = umma_desc_k_sw128(smem_u32(smem + L::oQ));
-      const uint64_t desc_k = umma_desc_k_sw128(smem_u32(smem + L::oKV));
-      const uint64_t desc_v = umma_desc_mn_sw128(smem_u32(smem + L::oKV), kHalfBytes);
-      uint32_t slot = 0, slot_ph = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, cn = 0;
+      const int page = 1 << a.c_.page_shift;
+      const int box = min(page, kTileKeys);         // rows per copy
+      const int copies = kTileKeys / box * L::kHalves;  // per step and operand
+      uint32_t slot = 0, slot_ph = 0, qn[2] = {0, 0};
       bool ok = true;
-      auto wait = [&](uint64_t* b, uint32_t ph) { return ok = ok && mbar_wait(b, ph, abort_flag, kDevTimeoutMma); };
-      auto next_slot = [&] {
-        if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
-      };
-      auto scores = [&](int x, uint32_t ks) {
-        const uint64_t dq = desc_q + (uint64_t)(x * (L::kTile >> 4)), dk = desc_k + (uint64_t)(ks * (L::kTile >> 4));
+      for (int i = 0; ok; ++i) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&it_full[i & 1], (i >> 1) & 1, abort_flag, kDevTimeoutProducer))) break;
+        const Item it = item_at(i);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&it_empty[i & 1]);
+        if (it.done) break;
+        const int32_t* table = a.b.table + (long long)it.seq * a.b.ldt;
+        const int end = max(it.endA, it.endB);
+        // this lane's copy of a step: its page is looked up one step ahead
+        const int half = lane & (L::kHalves - 1), r = lane / L::kHalves * box;
+        auto lookup = [&](int j) {
+          const int key = j * kTileKeys + r;
+          int pg = a.c_.n_pages;  // past the keys that exist: zeros, from outside the map
+          if (lane < copies && key < it.kv_end) {
+            const int e = table[key >> a.c_.page_shift];
+            if (e >= 0 && e < a.c_.n_pages) pg = e;
+            else note_bad_page();
+          }
+          return pg;
+        };
+        auto load = [&](const CUtensorMap* tm, int j, int pg) {
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_idle(&kv_empty[slot], slot_ph ^ 1, abort_flag, kDevTimeoutProducer, kWaitLimitNs));
+          if (!ok) return;
+          if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], L::kTile);
+          __syncwarp();
+          if (lane < copies)
+            tma_load_3d(smem + L::oKV + slot * L::kTile + half * (L::kTile / L::kHalves) + r * 128, tm, &kv_full[slot],
+                        64 * half, (it.kvh << a.c_.page_shift) + ((j * kTileKeys + r) & (page - 1)), pg);
+          __syncwarp();
+          if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
+        };
+        int pg = it.j0 < end ? lookup(it.j0) : 0;
+#pragma unroll 1
+        for (int j = it.j0; j < end && ok; ++j) {
+          const int pg_next = j + 1 < end ? lookup(j + 1) : 0;
+          load(&tmK, j, pg);
+          if (j == it.j0) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
-          umma_bf16_ss(tmem + kS + 128u * x, dq + off, dk + off, idesc_qk, k > 0);
+            for (int x = 0; x < 2; ++x) {
+              if (!ok || (x ? it.endB : it.endA) <= it.j0) continue;
+              ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[x], (qn[x] & 1) ^ 1, abort_flag, kDevTimeoutProducer));
+              if (!ok) continue;
+              ++qn[x];
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&q_full[x], a.tokens * a.group * D * 2);
+                for (int h = 0; h < L::kHalves; ++h)
+                  tma_load_3d(smem + L::oQ + x * L::kTile + h * (L::kTile / L::kHalves), &tmQ, &q_full[x], 64 * h,
+                              it.kvh * a.group, it.row0 + x * a.tokens);
+              }
+              __syncwarp();
+            }
+          }
+          if (ok) load(&tmV, j, pg);
+          pg = pg_next;
         }
-      };
-      auto values = [&](int x, uint32_t vs, bool acc, int half) {
-        const uint64_t dv = desc_v + (uint64_t)(vs * (L::kTile >> 4));
+      }
+    } else if (warp == 9) {
+      // ---------------------------------------------------------------- MMAs
+      // One thread runs the whole loop: the tensor core takes a step's 32 MMAs
+      // about as fast as they are issued, so what the issuing thread spends
+      // between them on waits and votes leaves the tensor core idle (with the
+      // whole warp waiting and electing a lane each time, a step of two tiles
+      // took 3400 cycles, 2048 of them MMAs).
+      if (elect_one()) {
+        const uint32_t idesc_qk = umma_idesc_bf16(128, kTileKeys, false, a.neg);
+        constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D, true, false);
+        constexpr int kHalfBytes = L::kTile / L::kHalves;
+        const uint64_t desc_q = umma_desc_k_sw128(smem_u32(smem + L::oQ));
+        const uint64_t desc_k = umma_desc_k_sw128(smem_u32(smem + L::oKV));
+        const uint64_t desc_v = umma_desc_mn_sw128(smem_u32(smem + L::oKV), kHalfBytes);
+        uint32_t slot = 0, slot_ph = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, cn = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t* b, uint32_t ph) { return ok = ok && mbar_wait(b, ph, abort_flag, kDevTimeoutMma); };
+        auto next_slot = [&] {
+          if (++slot == L::kSlots) slot = 0, slot_ph ^= 1;
+        };
+        auto scores = [&](int x, uint32_t ks) {
+          const uint64_t dq = desc_q + (uint64_t)(x * (L::kTile >> 4)), dk = desc_k + (uint64_t)(ks * (L::kTile >> 4));
 #pragma unroll
-        for (int k = half * 4; k < half * 4 + 4; ++k)
-          umma_bf16_ts(tmem + kO + (uint32_t)(D * x), tmem + kS + 128u * x + 8u * k, dv + (uint64_t)(128 * k), idesc_pv,
-                       acc || k > 0);
-      };
-      // An item's first scores are issued as soon as the previous item leaves
-      // room, in front of its other tile's last products where they can be.
-      struct Steps {
-        int done, j0, endA, endB, kv_end;
-        __device__ int last(int x) const { return x ? endB : endA; }
-        __device__ int end() const { return max(endA, endB); }
-      };
-      int n_read = 0;
-      auto read_item = [&](Steps& t) {
-        const Item& it = item_at(n_read);
-        t.done = it.done, t.j0 = it.j0, t.endA = it.endA, t.endB = it.endB, t.kv_end = it.kv_end;
-        mbar_arrive(&it_empty[n_read & 1]);
-        ++n_read;
-      };
-      auto first_scores = [&](const Steps& t, int x) {
-        ++qn[x];
-        tc_fence_after();
-        scores(x, slot);
-        umma_commit<1>(&s_full[x]);
-        if (t.j0 + 1 == t.last(x)) umma_commit<1>(&q_empty[x]);
-      };
-      Steps cur, nxt;
-      bool have = false;              // nxt holds the next item
-      bool given[2] = {false, false};  // its first scores are issued
-      while (ok) {
-        if (have) {
-          cur = nxt;
-          have = false;
-        } else {
-          if (!wait(&it_full[n_read & 1], (n_read >> 1) & 1)) break;
-          read_item(cur);
-        }
-        if (cur.done) break;
-        const int end = cur.end();
-        if (end <= cur.j0) continue;
-        if (!wait(&kv_full[slot], slot_ph)) break;
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
+            umma_bf16_ss(tmem + kS + 128u * x, dq + off, dk + off, idesc_qk, k > 0);
+          }
+        };
+        auto values = [&](int x, uint32_t vs, bool acc, int half) {
+          const uint64_t dv = desc_v + (uint64_t)(vs * (L::kTile >> 4));
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!given[x] && cur.j0 < cur.last(x) && wait(&q_full[x], qn[x] & 1)) first_scores(cur, x);
-          given[x] = false;
-        }
-        if (!ok) break;
-        umma_commit<1>(&kv_empty[slot]);
-        next_slot();
-        for (int j = cur.j0; j < end; ++j) {
-          const uint32_t vs = slot;
+          for (int k = half * 4; k < half * 4 + 4; ++k)
+            umma_bf16_ts(tmem + kO + (uint32_t)(D * x), tmem + kS + 128u * x + 8u * k, dv + (uint64_t)(128 * k), idesc_pv,
+                         acc || k > 0);
+        };
+        // An item's first scores are issued as soon as the previous item leaves
+        // room, in front of its other tile's last products where they can be.
+        struct Steps {
+          int done, j0, endA, endB, kv_end;
+          __device__ int last(int x) const { return x ? endB : endA; }
+          __device__ int end() const { return max(endA, endB); }
+        };
+        int n_read = 0;
+        auto read_item = [&](Steps& t) {
+          const Item& it = item_at(n_read);
+          t.done = it.done, t.j0 = it.j0, t.endA = it.endA, t.endB = it.endB, t.kv_end = it.kv_end;
+          mbar_arrive(&it_empty[n_read & 1]);
+          ++n_read;
+        };
+        auto first_scores = [&](const Steps& t, int x) {
+          ++qn[x];
+          tc_fence_after();
+          scores(x, slot);
+          umma_commit<1>(&s_full[x]);
+          if (t.j0 + 1 == t.last(x)) umma_commit<1>(&q_empty[x]);
+        };
+        Steps cur, nxt;
+        bool have = false;              // nxt holds the next item
+        bool given[2] = {false, false};  // its first scores are issued
+        while (ok) {
+          if (have) {
+            cur = nxt;
+            have = false;
+          } else {
+            if (!wait(&it_full[n_read & 1], (n_read >> 1) & 1)) break;
+            read_item(cur);
+          }
+          if (cur.done) break;
+          const int end = cur.end();
+          if (end <= cur.j0) continue;
           if (!wait(&kv_full[slot], slot_ph)) break;
-          next_slot();
-          const uint32_t ks = slot;
-          bool ahead = false;  // the next item's first keys have landed
-          if (j + 1 < end) {
-            if (!wait(&kv_full[slot], slot_ph)) break;
-            next_slot();
-          } else if (mbar_try_wait(&it_full[n_read & 1], (n_read >> 1) & 1)) {
-            read_item(nxt);
-            have = true;
-            ahead = !nxt.done && nxt.j0 < nxt.end() && mbar_try_wait(&kv_full[slot], slot_ph);
-          }
-          if (cur.kv_end - j * kTileKeys < kTileKeys) {  // values that do not exist: see the helper warp
-            clean_req[0] = (int)vs;
-            clean_req[1] = cur.kv_end - j * kTileKeys;
-            mbar_arrive(clean_ask);
-            if (!wait(clean_done, cn++ & 1)) break;
-          }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int last = cur.last(x);
-            if (j < last) {
-              if (!wait(&p_half[x], pn[x] & 1)) continue;
-              tc_fence_after();
-              values(x, vs, j > cur.j0, 0);
-              if (!wait(&p_full[x], pn[x] & 1)) continue;
-              ++pn[x];
-              tc_fence_after();
-              values(x, vs, true, 1);
-              if (j + 1 < last) {
-                scores(x, ks);
-                umma_commit<1>(&s_full[x]);
-                if (j + 2 == last) umma_commit<1>(&q_empty[x]);
-              } else {
-                umma_commit<1>(&o_full[x]);
-              }
-            }
-            if (ahead && nxt.j0 < nxt.last(x) && mbar_try_wait(&q_full[x], qn[x] & 1)) {
-              first_scores(nxt, x);
-              given[x] = true;
-            }
+            if (!given[x] && cur.j0 < cur.last(x) && wait(&q_full[x], qn[x] & 1)) first_scores(cur, x);
+            given[x] = false;
           }
           if (!ok) break;
-          umma_commit<1>(&kv_empty[vs]);
-          if (j + 1 < end) umma_commit<1>(&kv_empty[ks]);
+          umma_commit<1>(&kv_empty[slot]);
+          next_slot();
+          for (int j = cur.j0; j < end; ++j) {
+            const uint32_t vs = slot;
+            if (!wait(&kv_full[slot], slot_ph)) break;
+            next_slot();
+            const uint32_t ks = slot;
+            bool ahead = false;  // the next item's first keys have landed
+            if (j + 1 < end) {
+              if (!wait(&kv_full[slot], slot_ph)) break;
+              next_slot();
+            } else if (mbar_try_wait(&it_full[n_read & 1], (n_read >> 1) & 1)) {
+              read_item(nxt);
+              have = true;
+              ahead = !nxt.done && nxt.j0 < nxt.end() && mbar_try_wait(&kv_full[slot], slot_ph);
+            }
+            if (cur.kv_end - j * kTileKeys < kTileKeys) {  // values that do not exist: see the helper warp
+              clean_req[0] = (int)vs;
+              clean_req[1] = cur.kv_end - j * kTileKeys;
+              mbar_arrive(clean_ask);
+              if (!wait(clean_done, cn++ & 1)) break;
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int last = cur.last(x);
+              if (j < last) {
+                if (!wait(&p_half[x], pn[x] & 1)) continue;
+                tc_fence_after();
+                values(x, vs, j > cur.j0, 0);
+                if (!wait(&p_full[x], pn[x] & 1)) continue;
+                ++pn[x];
+                tc_fence_after();
+                values(x, vs, true, 1);
+                if (j + 1 < last) {
+                  scores(x, ks);
+                  umma_commit<1>(&s_full[x]);
+                  if (j + 2 == last) umma_commit<1>(&q_empty[x]);
+                } else {
+                  umma_commit<1>(&o_full[x]);
+                }
+              }
+              if (ahead && nxt.j0 < nxt.last(x) && mbar_try_wait(&q_full[x], qn[x] & 1)) {
+                first_scores(nxt, x);
+                given[x] = true;
+              }
+            }
+            if (!ok) break;
+            umma_commit<1>(&kv_empty[vs]);
+            if (j + 1 < end) umma_commit<1>(&kv_empty[ks]);
+          }
         }
+        // every MMA issued has completed before TMEM and shared memory are freed
+        umma_commit<1>(drain);
+        mbar_wait(drain, 0, nullptr, kDevTimeoutMma);
+        clean_req[0] = -1;
+        mbar_arrive(clean_ask);
       }
-      // every MMA issued has completed before TMEM and shared memory are freed
-      umma_commit<1>(drain);
-      mbar_wait(drain, 0, nullptr, kDevTimeoutMma);
-      clean_req[0] = -1;
-      mbar_arrive(clean_ask);
-    }
-    __syncwarp();
-  } else if (warp == 10) {
-    // -------------------------------------------------------------- helper
-    // Rows of V behind the last key, up to the end of its page, may hold
-    // anything, and a zero weight times a NaN is one: on the MMA thread's
-    // request they are zeroed once they have landed.
-    constexpr int kHalfBytes = L::kTile / L::kHalves;
-    for (uint32_t n = 0;; ++n) {
-      // lasts as long as the kernel does: the MMA thread, whose own waits are
-      // bounded, always ends it
-      if (!__all_sync(0xffffffffu, mbar_wait_idle(clean_ask, n & 1, abort_flag, kDevTimeoutMma, 100 * kWaitLimitNs))) break;
-      const int vs = clean_req[0], have = clean_req[1];
       __syncwarp();
-      if (vs < 0) break;
-      const int upto = min(kTileKeys, (have + (1 << a.c_.page_shift) - 1) >> a.c_.page_shift << a.c_.page_shift);
-      const int chunks = (upto - have) * (D / 8);
-      for (int e = lane; e < chunks; e += 32) {
-        const int r = have + e / (D / 8), c = e % (D / 8);
-        *reinterpret_cast<uint4*>(smem + L::oKV + vs * L::kTile + (c >> 3) * kHalfBytes + r * 128 + (c & 7) * 16) =
-            make_uint4(0, 0, 0, 0);
+    } else if (warp == 10) {
+      // -------------------------------------------------------------- helper
+      // Rows of V behind the last key, up to the end of its page, may hold
+      // anything, and a zero weight times a NaN is one: on the MMA thread's
+      // request they are zeroed once they have landed.
+      constexpr int kHalfBytes = L::kTile / L::kHalves;
+      for (uint32_t n = 0;; ++n) {
+        // lasts as long as the kernel does: the MMA thread, whose own waits are
+        // bounded, always ends it
+        if (!__all_sync(0xffffffffu, mbar_wait_idle(clean_ask, n & 1, abort_flag, kDevTimeoutMma, 100 * kWaitLimitNs))) break;
+        const int vs = clean_req[0], have = clean_req[1];
+        __syncwarp();
+        if (vs < 0) break;
+        const int upto = min(kTileKeys, (have + (1 << a.c_.page_shift) - 1) >> a.c_.page_shift << a.c_.page_shift);
+        const int chunks = (upto - have) * (D / 8);
+        for (int e = lane; e < chunks; e += 32) {
+          const int r = have + e / (D / 8), c = e % (D / 8);
+          *reinterpret_cast<uint4*>(smem + L::oKV + vs * L::kTile + (c >> 3) * kHalfBytes + r * 128 + (c & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(clean_done);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(clean_done);
+    } else {
+      // ----------------------------------------------------------- scheduling
+      // Decodes the CTA's work items ahead of their use.
+      grid_dep_wait();
+      grid_dep_launch();
+      ShareWalk walk;
+      Pairs mine = {0, 0, 0, 0, 0};
+      if (a.shares) walk.init(a, lane);
+      else if (a.b.batch <= 32) mine = load_pairs(a, lane);
+      for (int i = 0;; ++i) {
+        Item it;
+        it.done = 1;
+        if (a.shares) {
+          if (!walk.next(a, it)) it.done = 1;
+        } else {
+          // every other round backwards: the items come in falling cost, so that
+          // each CTA's sum stays near the mean
+          ranked_item(a, mine, i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, it);
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait_idle(&it_empty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag,
+                                                    kDevTimeoutProducer, 100 * kWaitLimitNs)))
+          break;
+        if (lane == 0) {
+          item_at(i) = it;
+          mbar_arrive(&it_full[i & 1]);
+        }
+        if (it.done) break;
+      }
     }
-  } else {
-    // ----------------------------------------------------------- scheduling
-    // Decodes the CTA's work items ahead of their use.
-    grid_dep_wait();
-    grid_dep_launch();
-    ShareWalk walk;
-    Pairs mine = {0, 0, 0, 0, 0};
-    if (a.shares) walk.init(a, lane);
-    else if (a.b.batch <= 32) mine = load_pairs(a, lane);
-    for (int i = 0;; ++i) {
-      Item it;
-      it.done = 1;
-      if (a.shares) {
-        if (!walk.next(a, it)) it.done = 1;
-      } else {
-        // every other round backwards: the items come in falling cost, so that
-        // each CTA's sum stays near the mean
-        ranked_item(a, mine, i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, it);
-      }
-      if (!__all_sync(0xffffffffu, mbar_wait_idle(&it_empty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag,
-                                                  kDevTimeoutProducer, 100 * kWaitLimitNs)))
-        break;
-      if (lane == 0) {
-        item_at(i) = it;
-        mbar_arrive(&it_full[i & 1]);
-      }
-      if (it.done) break;
-    }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ------------------------------------------------------------- softmax
