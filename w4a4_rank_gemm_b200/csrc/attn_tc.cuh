@@ -49,6 +49,7 @@ struct TcArgs {
   float c;           // |scale| log2 e, never 0
   int neg;           // scale < 0: the product is taken with -Q
   int T, n_heads, group, tokens;  // tokens: per tile, 128 / group
+  int pair_shift;    // log2 of a pair's tokens, or -1
   int shares;        // > 0: equal shares of the work for that many CTAs; 0: whole items
   int prefix;        // > 0: decode rows; every row is at sequence 0's first `prefix` keys, up to its own kv_len
   BatchArgs b;
@@ -130,6 +131,12 @@ struct Pairs {
   int keys;          // of kv, those that the page table holds
 };
 
+// n / (2 tokens), n >= 0; by a shift where it can be (the scheduler's counting
+// divides often, and a work item waits for it).
+__device__ __forceinline__ int div_pair(const TcArgs& a, int n) {
+  return a.pair_shift >= 0 ? n >> a.pair_shift : n / (2 * a.tokens);
+}
+
 __device__ __forceinline__ Pairs load_pairs(const TcArgs& a, int b) {
   const int pair = 2 * a.tokens;
   Pairs s = {0, 0, 0, 0, 0};
@@ -137,7 +144,7 @@ __device__ __forceinline__ Pairs load_pairs(const TcArgs& a, int b) {
     s.first = a.b.cu_q[b];
     s.n = max(0, a.b.cu_q[b + 1] - s.first);
     s.kv = a.b.kv_len[b];
-    s.np = ceil_div(s.n, pair);
+    s.np = div_pair(a, s.n + pair - 1);
     s.keys = max(0, min(s.kv, a.b.max_pages << a.c_.page_shift));
   }
   return s;
@@ -189,7 +196,7 @@ __device__ __forceinline__ void ranked_item(const TcArgs& a, const Pairs& mine, 
       if (x <= 0) return mine.np;
       const int v = (x - 1) * kTileKeys;
       if (mine.np == 0 || min(mine.keys, mine.kv) <= v) return 0;
-      return mine.np - min(mine.np, max(0, v - (mine.kv - mine.n)) / pair);
+      return mine.np - min(mine.np, div_pair(a, max(0, v - (mine.kv - mine.n))));
     };
     int x = 0;
     if (total * heads > (int)gridDim.x) {
@@ -931,6 +938,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // 64 columns at a time through the warp's 4 KB of shared memory, so that
         // rows leave as whole 128-byte lines (16-byte chunks swizzled by the row)
         __nv_bfloat16* dst = valid ? a.o + (long long)t * a.ldo + (long long)h * D : nullptr;
+        __nv_bfloat16* to[8];  // the rows that this lane stores 16 bytes of
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          to[e] = reinterpret_cast<__nv_bfloat16*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), 4 * e + (lane >> 3)));
 #pragma unroll 1
         for (int q = 0; q < D / 64; ++q) {
           uint32_t o[2][32];
@@ -957,10 +969,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int rr = 4 * e + (lane >> 3), ch = lane & 7;
-            __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), rr));
             const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
-            if (to != nullptr) *reinterpret_cast<uint4*>(to + 64 * q + 8 * ch) = v;
+            if (to[e] != nullptr) *reinterpret_cast<uint4*>(to[e] + 64 * q + 8 * ch) = v;
           }
           __syncwarp();
         }

@@ -2050,6 +2050,13 @@ serq_status check_ws(const void* ws, size_t have, size_t need) {
 
 namespace {
 
+// log2 of a tile pair's tokens, -1 when that is no power of two.
+int pair_shift(int tokens) {
+  int s = 1;
+  while ((1 << s) < 2 * tokens) ++s;
+  return (1 << s) == 2 * tokens ? s : -1;
+}
+
 // Tile pairs per kv head that a prompt call can have at most, its work split
 // and workspace.  Whole items balance well once there are two per SM; with
 // fewer, equal shares do (whose cut items cost a pass to join them): below one
@@ -2119,6 +2126,7 @@ serq_status serq_attn_prefill(const serq_kv_cache* cache, const void* Q, int ldq
   a.n_heads = n_heads;
   a.group = p.group;
   a.tokens = p.tokens;
+  a.pair_shift = pair_shift(p.tokens);
   a.shares = p.shares;
   a.prefix = 0;
   a.b = {cu_q, kv_len, page_table, batch, max_pages, ld_table};
@@ -2232,6 +2240,7 @@ serq_status serq_attn_decode(const serq_kv_cache* cache, const void* Q, int ldq,
     a.n_heads = n_heads;
     a.group = p.group;
     a.tokens = p.tokens;
+    a.pair_shift = pair_shift(p.tokens);
     a.shares = p.pshares;
     a.prefix = p.prefix;
     a.b = d.b;
