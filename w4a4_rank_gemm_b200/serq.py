@@ -686,51 +686,56 @@ class KVCache:
             pass
 
 
-def _token_rows(t: torch.Tensor, name: str, cache: KVCache, rows: Optional[int] = None, heads: Optional[int] = None):
+_BF16, _I32 = torch.bfloat16, torch.int32
+_rope_append, _attn_prefill, _attn_decode = lib.serq_rope_append, lib.serq_attn_prefill, lib.serq_attn_decode
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+# A decode step's launches take the GPU a few microseconds each, about what a
+# call from Python takes: the checks below ask torch for as little as they can.
+def _token_rows(t: torch.Tensor, name: str, cache: KVCache, rows: int = -1, heads: int = -1):
     """Checks bf16 token rows of whole heads on the cache's device; returns
-    rows, heads and row stride.  (These checks run once per tensor and call:
-    as few calls into torch as they can be written with.)"""
-    if t.dtype is not torch.bfloat16 or t.dim() != 2 or t.get_device() != cache.index:
+    rows, heads and row stride."""
+    shape = t.shape
+    if len(shape) != 2 or t.dtype is not _BF16 or t.get_device() != cache.index:
         raise ValueError(f"{name} must be a 2-D bf16 tensor on the cache's device")
-    n, cols = t.shape
+    n, cols = shape
     ld, unit = t.stride()
-    h = cols // cache.head_dim
-    if unit != 1 or h * cache.head_dim != cols or h == 0 or (heads is not None and h != heads):
-        raise ValueError(f"{name} must hold {'whole' if heads is None else heads} heads of {cache.head_dim} with unit "
+    h, rest = divmod(cols, cache.head_dim)
+    if unit != 1 or rest or h == 0 or (heads >= 0 and h != heads):
+        raise ValueError(f"{name} must hold {'whole' if heads < 0 else heads} heads of {cache.head_dim} with unit "
                          f"column stride (its rows have {cols} columns)")
-    if rows is not None and n != rows:
+    if rows >= 0 and n != rows:
         raise ValueError(f"{name} has {n} rows, not {rows}")
     return n, h, ld if n > 1 else cols
 
 
 def _batch_args(cache: KVCache, kv_len: torch.Tensor, page_table: torch.Tensor, cu_q: Optional[torch.Tensor] = None):
-    i32, index = torch.int32, cache.index
-    if kv_len.dtype is not i32 or kv_len.dim() != 1 or kv_len.get_device() != index or not kv_len.is_contiguous():
+    index = cache.index
+    shape = kv_len.shape
+    if len(shape) != 1 or kv_len.dtype is not _I32 or kv_len.get_device() != index or kv_len.stride(0) != 1:
         raise ValueError("kv_len must be a dense 1-D int32 tensor on the cache's device")
-    B = kv_len.shape[0]
-    if page_table.dtype is not i32 or page_table.dim() != 2 or page_table.get_device() != index:
+    B = shape[0]
+    shape = page_table.shape
+    if len(shape) != 2 or page_table.dtype is not _I32 or page_table.get_device() != index:
         raise ValueError("page_table must be a 2-D int32 tensor on the cache's device")
-    n, cols = page_table.shape
+    n, cols = shape
     ld, unit = page_table.stride()
     if n != B or (unit != 1 and cols > 1):
         raise ValueError("page_table needs a row with unit column stride for each sequence")
-    if cu_q is not None and (cu_q.dtype is not i32 or cu_q.dim() != 1 or cu_q.get_device() != index or
-                             cu_q.shape[0] != B + 1 or not cu_q.is_contiguous()):
-        raise ValueError("cu_q must be a dense 1-D int32 tensor of one entry more than sequences on the cache's device")
+    if cu_q is not None:
+        shape = cu_q.shape
+        if (len(shape) != 1 or shape[0] != B + 1 or cu_q.dtype is not _I32 or cu_q.get_device() != index
+                or cu_q.stride(0) != 1):
+            raise ValueError("cu_q must be a dense 1-D int32 tensor of one entry more than sequences on the cache's "
+                             "device")
     return B, cols, ld if B > 1 else cols
 
 
-def _call(cache: KVCache, stream, where: str, f, *args):
-    """Runs f(*args, stream) with the cache's device current, on its current
-    stream unless one is given."""
-    st = torch._C._cuda_getCurrentRawStream(cache.index) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == cache.index:
-        status = f(*args, st)
-    else:
-        with torch.cuda.device(cache.index):
-            status = f(*args, st)
-    if status != OK:
-        raise SerqError(status, where)
+def _elsewhere(cache: KVCache, f, *args) -> int:
+    """f(*args) with the cache's device current, for callers on another one."""
+    with torch.cuda.device(cache.index):
+        return f(*args)
 
 
 def _scratch(n: int, cache: KVCache, stream) -> Optional[torch.Tensor]:
@@ -742,7 +747,7 @@ def _scratch(n: int, cache: KVCache, stream) -> Optional[torch.Tensor]:
 
 
 def _check_ws(ws: torch.Tensor, cache: KVCache) -> torch.Tensor:
-    if ws.dtype is not torch.uint8 or not ws.is_contiguous() or ws.get_device() != cache.index:
+    if ws.dtype is not torch.uint8 or ws.get_device() != cache.index or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous uint8 tensor on the cache's device")
     return ws
 
@@ -763,8 +768,8 @@ def rope_append(rope: Rope, cache: KVCache, Q: torch.Tensor, K: torch.Tensor, V:
     T, n_heads, ldq = _token_rows(Q, "Q", cache)
     ldk = _token_rows(K, "K", cache, T, cache.n_kv_heads)[2]
     ldv = _token_rows(V, "V", cache, T, cache.n_kv_heads)[2]
-    for w in (q_weight, k_weight):
-        if w is not None and (w.dtype is not torch.bfloat16 or w.shape != (cache.head_dim,) or not w.is_contiguous()
+    for w in (q_weight, k_weight) if q_weight is not None or k_weight is not None else ():
+        if w is not None and (w.dtype is not _BF16 or w.shape != (cache.head_dim,) or not w.is_contiguous()
                               or w.get_device() != cache.index):
             raise ValueError("norm weights must be contiguous bf16 tensors of head_dim elements")
     if cu_q is None:
@@ -773,10 +778,13 @@ def rope_append(rope: Rope, cache: KVCache, Q: torch.Tensor, K: torch.Tensor, V:
     if Qout is None:
         Qout = _out_like(Q, stream)
     ldo = _token_rows(Qout, "Qout", cache, T, n_heads)[2]
-    _call(cache, stream, "serq_rope_append", lib.serq_rope_append, rope.handle, cache.handle, Q.data_ptr(), ldq,
-          K.data_ptr(), ldk, V.data_ptr(), ldv, T, n_heads, None if q_weight is None else q_weight.data_ptr(),
-          None if k_weight is None else k_weight.data_ptr(), eps, B, cu_q.data_ptr(), kv_len.data_ptr(),
-          page_table.data_ptr(), cols, ldt, Qout.data_ptr(), ldo)
+    args = (rope._h, cache._h, Q.data_ptr(), ldq, K.data_ptr(), ldk, V.data_ptr(), ldv, T, n_heads,
+            None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps, B,
+            cu_q.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), cols, ldt, Qout.data_ptr(), ldo,
+            _raw_stream(cache.index) if stream is None else stream.cuda_stream)
+    status = (_rope_append(*args) if _current_device() == cache.index else _elsewhere(cache, _rope_append, *args))
+    if status != OK:
+        raise SerqError(status, "serq_rope_append")
     return Qout
 
 
@@ -816,10 +824,13 @@ def attn_prefill(cache: KVCache, Q: torch.Tensor, cu_q: torch.Tensor, kv_len: to
         ws = _scratch(_ws_bytes(cache, lib.serq_attn_prefill_ws_bytes, T, n_heads, B, cols, max_kv), cache, stream)
     else:
         _check_ws(ws, cache)
-    _call(cache, stream, "serq_attn_prefill", lib.serq_attn_prefill, cache.handle, Q.data_ptr(), ldq, T, n_heads,
-          cache.default_scale if scale is None else scale, B, cu_q.data_ptr(), kv_len.data_ptr(),
-          page_table.data_ptr(), cols, ldt, max_kv, None if ws is None else ws.data_ptr(),
-          0 if ws is None else ws.numel(), O.data_ptr(), ldo)
+    args = (cache._h, Q.data_ptr(), ldq, T, n_heads, cache.default_scale if scale is None else scale, B,
+            cu_q.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), cols, ldt, max_kv,
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), O.data_ptr(), ldo,
+            _raw_stream(cache.index) if stream is None else stream.cuda_stream)
+    status = (_attn_prefill(*args) if _current_device() == cache.index else _elsewhere(cache, _attn_prefill, *args))
+    if status != OK:
+        raise SerqError(status, "serq_attn_prefill")
     return O
 
 
@@ -838,9 +849,13 @@ def attn_decode(cache: KVCache, Q: torch.Tensor, kv_len: torch.Tensor, page_tabl
                       stream)
     else:
         _check_ws(ws, cache)
-    _call(cache, stream, "serq_attn_decode", lib.serq_attn_decode, cache.handle, Q.data_ptr(), ldq, n_heads,
-          cache.default_scale if scale is None else scale, B, kv_len.data_ptr(), page_table.data_ptr(), cols, ldt,
-          prefix_len, max_kv, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), O.data_ptr(), ldo)
+    args = (cache._h, Q.data_ptr(), ldq, n_heads, cache.default_scale if scale is None else scale, B,
+            kv_len.data_ptr(), page_table.data_ptr(), cols, ldt, prefix_len, max_kv,
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), O.data_ptr(), ldo,
+            _raw_stream(cache.index) if stream is None else stream.cuda_stream)
+    status = (_attn_decode(*args) if _current_device() == cache.index else _elsewhere(cache, _attn_decode, *args))
+    if status != OK:
+        raise SerqError(status, "serq_attn_decode")
     return O
 
 
