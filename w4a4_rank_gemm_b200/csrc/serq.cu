@@ -2073,7 +2073,8 @@ PrefillPlan prefill_plan(const serq_kv_cache* c, int T, int n_heads, int batch, 
   PrefillPlan p;
   p.group = n_heads / c->n_kv_heads;
   p.tokens = serq::attn::kTileRows / p.group;
-  p.pairs = T / (2 * p.tokens) + std::min(batch, T);
+  const long long pair = 2 * p.tokens;
+  p.pairs = std::min(T / pair + std::min(batch, T), (T + batch * (pair - 1)) / pair);
   const long long cap = (long long)max_pages * c->page_size, items = p.pairs * c->n_kv_heads, sms = sm_count();
   const long long keys = max_kv ? std::min<long long>(max_kv, cap) : cap;
   const bool share = keys > 512 && (items < sms || (items < 2 * sms && keys * batch >= 3ll * T));
