@@ -323,25 +323,24 @@ struct ShareWalk {
   int seq, kvh, tile;
   Pairs s;
 
-  // `one`: the lane's sequence when the batch fits a warp (or the prefix's).
-  __device__ void init(const TcArgs& a, int lane) {
-    const int heads = a.c_.n_kv_heads;
-    long long before = 0, total;
-    if (a.prefix) {
-      s = prefix_pairs(a, lane);
-      total = measure(a, s).before(s.np);
-    } else {
-      share_sums(a, 0, lane, before, total);
+  // All work there is (the warp calls, and locate).
+  __device__ long long total(const TcArgs& a, int lane) {
+    if (a.prefix == 0) {
+      long long before, all;
+      share_sums(a, 0, lane, before, all);
+      return all * a.c_.n_kv_heads;
     }
-    total *= heads;
-    const Shares shares(total, a.shares);
-    x = shares.start(blockIdx.x);
-    x1 = shares.start(blockIdx.x + 1);
-    if (x >= x1) return;
+    s = prefix_pairs(a, lane);
+    return measure(a, s).before(s.np) * a.c_.n_kv_heads;
+  }
+
+  // The item that holds unit `at` of the work.
+  __device__ void locate(const TcArgs& a, long long at, int lane) {
+    const int heads = a.c_.n_kv_heads;
     seq = 0;
     long long base = 0, per_head = 0;
     if (a.prefix) {
-      per_head = quotient(total, heads);
+      per_head = measure(a, s).before(s.np);
     } else {
       for (int b0 = 0;; b0 += 32) {
         const Pairs p = load_pairs(a, b0 + lane);
@@ -352,7 +351,7 @@ struct ShareWalk {
           const long long v = __shfl_up_sync(0xffffffffu, incl, d);
           if (lane >= d) incl += v;
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, x < (base + incl) * heads);
+        const uint32_t hit = __ballot_sync(0xffffffffu, at < (base + incl) * heads);
         if (hit) {
           const int src = __ffs(hit) - 1;
           seq = b0 + src;
@@ -364,7 +363,7 @@ struct ShareWalk {
       }
       s = load_pairs(a, seq);
     }
-    const long long rest = x - base * heads;
+    const long long rest = at - base * heads;
     kvh = (int)quotient(rest, per_head);
     const long long in = rest - kvh * per_head;
     const Measure m = measure(a, s);
@@ -376,6 +375,13 @@ struct ShareWalk {
     }
     tile = lo;
     start = base * heads + kvh * per_head + m.before(lo);
+  }
+
+  __device__ void init(const TcArgs& a, int lane) {
+    const Shares shares(total(a, lane), a.shares);
+    x = shares.start(blockIdx.x);
+    x1 = shares.start(blockIdx.x + 1);
+    if (x < x1) locate(a, x, lane);
   }
 
   // False: the share is finished.  Segments without a step are passed over.
@@ -1016,12 +1022,16 @@ __device__ __forceinline__ void load_part(const float* p, bool take, float (&x)[
 
 // Joins the parts of items that shares cut:
 //   O = sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M),  s in share order.
-// One CTA per tile pair, kv head and 32 rows; 4 rows per warp.
-template <int D>
-__global__ void __launch_bounds__(256) k_merge(const TcArgs a) {
+// CTAs run over tile pairs, kv heads and (z) parts of a pair's rows; items that
+// are not cut leave at once.  Four rows of a warp are joined together, KP parts
+// at a time, all in flight together.
+template <int D, int KP>
+__global__ void __launch_bounds__(256, KP == 2 ? 2 : 1) k_merge(const TcArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // lengths and offsets are inputs of the call: k_attn lets this grid start
-  // only after its own wait, so they are complete here
+  // Lengths and offsets are inputs of the call: k_attn lets this grid start
+  // only after its own wait, so they are complete here.  (Every CTA waits
+  // before it leaves: what follows in the stream may rely on this grid's end
+  // for k_attn's.)
   const int pair = 2 * a.tokens, heads = a.c_.n_kv_heads, kvh = blockIdx.y;
   int seq = -1, tile = blockIdx.x;
   for (int b0 = 0; b0 < a.b.batch; b0 += 32) {
@@ -1041,8 +1051,6 @@ __global__ void __launch_bounds__(256) k_merge(const TcArgs a) {
     }
     tile -= __shfl_sync(0xffffffffu, incl, 31);
   }
-  // (Every CTA waits before it leaves: what follows in the stream may rely on
-  // this grid's end for k_attn's.)
   if (seq < 0) {
     grid_dep_wait();
     return;
@@ -1070,69 +1078,71 @@ __global__ void __launch_bounds__(256) k_merge(const TcArgs a) {
   grid_dep_wait();
   if (__any_sync(0xffffffffu, whole)) return;  // finished by its CTA
   constexpr int E = D / 32;
-  // the warp's four rows together, so that their parts are in flight together
-  long long at[4];  // output offset, -1: no row
-  float acc[4][E] = {}, z[4] = {}, top[4];
-  const int r0 = blockIdx.z * 32 + warp * 4;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + i, x = r >> 7, tok = (r & 127) / a.group, ti = x * a.tokens + tok;
-    const int t = s.first + tile * pair + ti;
-    const bool row = tok < a.tokens && ti < min(pair, s.n - tile * pair) && t >= 0 && t < a.T;
-    at[i] = row ? t * a.ldo + (long long)(kvh * a.group + (r & 127) - tok * a.group) * D : -1;
-    top[i] = -INFINITY;
-  }
-  if (at[0] < 0 && at[1] < 0 && at[2] < 0 && at[3] < 0) return;
-  for (int b0 = c0; b0 <= c1; b0 += 32) {
-    const int slot = part(b0 + lane);
-    float w[4];
+#pragma unroll 1
+  for (int g = blockIdx.z; g < 8; g += gridDim.z) {
+    long long at[4];  // output offset, -1: no row
+    float acc[4][E] = {}, z[4] = {}, top[4];
+    const int r0 = g * 32 + warp * 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float lse = slot >= 0 && at[i] >= 0 ? a.plse[(long long)slot * 256 + r0 + i] : -INFINITY;
-      float mx = lse;
-#pragma unroll
-      for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-      mx = fmaxf(mx, top[i]);
-      const float f = mx == -INFINITY ? 1.f : ex2(top[i] - mx);
-      top[i] = mx;
-      w[i] = lse == -INFINITY ? 0.f : ex2(lse - mx);
-      float zz = w[i];
-#pragma unroll
-      for (int d = 16; d; d >>= 1) zz += __shfl_xor_sync(0xffffffffu, zz, d);
-      z[i] = z[i] * f + zz;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[i][e] *= f;
+      const int r = r0 + i, x = r >> 7, tok = (r & 127) / a.group, ti = x * a.tokens + tok;
+      const int t = s.first + tile * pair + ti;
+      const bool row = tok < a.tokens && ti < min(pair, s.n - tile * pair) && t >= 0 && t < a.T;
+      at[i] = row ? t * a.ldo + (long long)(kvh * a.group + (r & 127) - tok * a.group) * D : -1;
+      top[i] = -INFINITY;
     }
-    const int cnt = min(32, c1 - b0 + 1);
-    for (int k1 = 0; k1 < cnt; k1 += 4) {
-      float v[4][4][E], wk[4][4];
+    if (at[0] < 0 && at[1] < 0 && at[2] < 0 && at[3] < 0) continue;
+    for (int b0 = c0; b0 <= c1; b0 += 32) {
+      const int slot = part(b0 + lane);
+      float w[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int sk = __shfl_sync(0xffffffffu, slot, (k1 + k) & 31);
-        const float* src = a.po + ((long long)sk * 256 + r0) * D + lane * E;
+      for (int i = 0; i < 4; ++i) {
+        const float lse = slot >= 0 && at[i] >= 0 ? a.plse[(long long)slot * 256 + r0 + i] : -INFINITY;
+        float mx = lse;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          wk[k][i] = __shfl_sync(0xffffffffu, w[i], (k1 + k) & 31);
-          if (k1 + k >= cnt) wk[k][i] = 0.f;
-          // an empty part's row is not written, nor read
-          load_part<E>(src + i * D, wk[k][i] != 0.f, v[k][i]);
-        }
+        for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        mx = fmaxf(mx, top[i]);
+        const float f = mx == -INFINITY ? 1.f : ex2(top[i] - mx);
+        top[i] = mx;
+        w[i] = lse == -INFINITY ? 0.f : ex2(lse - mx);
+        float zz = w[i];
+#pragma unroll
+        for (int d = 16; d; d >>= 1) zz += __shfl_xor_sync(0xffffffffu, zz, d);
+        z[i] = z[i] * f + zz;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[i][e] *= f;
       }
+      const int cnt = min(32, c1 - b0 + 1);
+      for (int k1 = 0; k1 < cnt; k1 += KP) {
+        float v[KP][4][E], wk[KP][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < KP; ++k) {
+          const int sk = __shfl_sync(0xffffffffu, slot, (k1 + k) & 31);
+          const float* src = a.po + ((long long)sk * 256 + r0) * D + lane * E;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i) {
+            wk[k][i] = __shfl_sync(0xffffffffu, w[i], (k1 + k) & 31);
+            if (k1 + k >= cnt) wk[k][i] = 0.f;
+            // an empty part's row is not written, nor read
+            load_part<E>(src + i * D, wk[k][i] != 0.f, v[k][i]);
+          }
+        }
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[i][e] += wk[k][i] * v[k][i][e];
+        for (int k = 0; k < KP; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[i][e] += wk[k][i] * v[k][i][e];
+      }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (at[i] < 0) continue;
-    const float inv = z[i] > 0.f ? 1.f / z[i] : 0.f;
-    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + at[i] + lane * E);
+    for (int i = 0; i < 4; ++i) {
+      if (at[i] < 0) continue;
+      const float inv = z[i] > 0.f ? 1.f / z[i] : 0.f;
+      __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + at[i] + lane * E);
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) dst[e] = __floats2bfloat162_rn(acc[i][2 * e] * inv, acc[i][2 * e + 1] * inv);
+      for (int e = 0; e < E / 2; ++e) dst[e] = __floats2bfloat162_rn(acc[i][2 * e] * inv, acc[i][2 * e + 1] * inv);
+    }
   }
 }
 
@@ -1167,9 +1177,12 @@ inline cudaError_t launch_tc(const CUtensorMap& tmQ, const CUtensorMap& tmK, con
 }
 
 template <int D>
-inline cudaError_t launch_merge(const TcArgs& a, int pairs, cudaStream_t st) {
+inline cudaError_t launch_merge(const TcArgs& a, int pairs, int sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pairs, a.c_.n_kv_heads, 8);
+  // a CTA's look-ups cost about as much as joining 64 rows: more CTAs per item,
+  // with more parts in flight, only where items are few (and have many parts)
+  const bool few = (long long)pairs * a.c_.n_kv_heads * 3 <= sms;
+  cfg.gridDim = dim3(pairs, a.c_.n_kv_heads, few ? 8 : 2);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1177,7 +1190,7 @@ inline cudaError_t launch_merge(const TcArgs& a, int pairs, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_merge<D>, a);
+  return few ? cudaLaunchKernelEx(&cfg, k_merge<D, 4>, a) : cudaLaunchKernelEx(&cfg, k_merge<D, 2>, a);
 }
 
 }  // namespace attn

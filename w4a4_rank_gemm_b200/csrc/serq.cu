@@ -2058,11 +2058,13 @@ int pair_shift(int tokens) {
 }
 
 // Tile pairs per kv head that a prompt call can have at most, its work split
-// and workspace.  Whole items balance well once there are two per SM; with
-// fewer, equal shares do (whose cut items cost a pass to join them): below one
-// item per SM always, up to two where the keys reach far in front of the rows,
-// so that all items cost about the same (256 items of prompts of 2048 tokens
-// pack to within 3% of the mean as they are).
+// and workspace.  Whole items balance well once there are two per SM, or when
+// prompts make them uneven.  Equal shares let idle SMs take part, at the price of
+// writing, reading and joining the cut items' parts.  They are taken when the
+// steps saved (of 128 keys; about 1.8 us) pay for that: 32 items of 48 steps
+// (40 tokens over 6000) 39 us, whole 78; 104 of up to 60 steps 79, whole 100; 32 of
+// 14 steps 22.6, whole 30.2; but 96 of 28 steps 68, whole 60; 128 of 35 steps 95,
+// whole 75; 19 of 5 steps 23.5, whole 16.6.
 struct PrefillPlan {
   int group, tokens, shares, ctas;
   bool longer;  // items of more than 16 steps: see k_attn's LONG
@@ -2077,7 +2079,9 @@ PrefillPlan prefill_plan(const serq_kv_cache* c, int T, int n_heads, int batch, 
   p.pairs = std::min(T / pair + std::min(batch, T), (T + batch * (pair - 1)) / pair);
   const long long cap = (long long)max_pages * c->page_size, items = p.pairs * c->n_kv_heads, sms = sm_count();
   const long long keys = max_kv ? std::min<long long>(max_kv, cap) : cap;
-  const bool share = keys > 512 && (items < sms || (items < 2 * sms && keys * batch >= 3ll * T));
+  // (items is a bound: a little above one per SM it may well be one)
+  const long long rounds = items * 7 < sms * 8 ? 1 : 2, saved = keys * (rounds * sms - items) / (128 * sms);
+  const bool share = items < 2 * sms && saved >= 5 + items / 10 && (rounds == 1 || keys * batch >= 3ll * T);
   p.shares = share ? serq::attn::tc_shares(items, keys, (int)sms) : 0;
   p.longer = keys > 2048;
   p.ctas = share ? p.shares : (int)std::min(items, sms);
@@ -2135,8 +2139,9 @@ serq_status serq_attn_prefill(const serq_kv_cache* cache, const void* Q, int ldq
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = D == 128 ? serq::attn::launch_tc<128>(tmQ, cache->tm[0][0], cache->tm[1][0], a, p.ctas, p.longer, st)
                            : serq::attn::launch_tc<64>(tmQ, cache->tm[0][0], cache->tm[1][0], a, p.ctas, p.longer, st);
-  if (e == cudaSuccess && p.shares)
-    e = D == 128 ? serq::attn::launch_merge<128>(a, (int)p.pairs, st) : serq::attn::launch_merge<64>(a, (int)p.pairs, st);
+  if (e == cudaSuccess && p.shares > 1)
+    e = D == 128 ? serq::attn::launch_merge<128>(a, (int)p.pairs, sm_count(), st)
+                 : serq::attn::launch_merge<64>(a, (int)p.pairs, sm_count(), st);
   if (e != cudaSuccess) return cuda_fail(e, "serq_attn_prefill launch");
   return ok();
 }
