@@ -612,7 +612,7 @@ serq_status serq_mx_linear(const serq_mx_layer* q, const void* Xq, const void* x
  *                      values to a paged cache;
  *   serq_attn_prefill  causal attention of packed prompts, or chunks of them,
  *                      over the cache;
- *   serq_attn_decode   one query per sequence over the cache, a prefix that
+ *   serq_attn_decode   one query per sequence over the cache, a long prefix that
  *                      all sequences share being read once for the batch.
  *
  * Rows of Q, K, V and O are token rows as the linears write them: bf16, head
@@ -754,9 +754,10 @@ serq_status serq_attn_prefill(const serq_kv_cache* cache, const void* Q, int ldq
  * kv_len[b] cached positions.
  *  prefix_len  >= 0, a multiple of page_size, <= max_pages page_size: the first
  *              prefix_len positions of every sequence are the same tokens, in
- *              the pages of page_table row 0.  They are read once for the whole
- *              batch; entries of other rows below prefix_len / page_size are
- *              not used.  kv_len[b] < prefix_len cuts sequence b's part of it.
+ *              the pages of page_table row 0; entries of other rows below
+ *              prefix_len / page_size are not used.  They are read once for the
+ *              whole batch, unless too little is saved by that (below 112 MB of
+ *              repeated reads).  kv_len[b] < prefix_len cuts sequence b's part.
  *  max_kv, ws  as above, with serq_attn_decode_ws_bytes.
  */
 size_t serq_attn_decode_ws_bytes(const serq_kv_cache* cache, int batch, int n_heads, int max_pages, int prefix_len,

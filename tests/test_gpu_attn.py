@@ -676,3 +676,70 @@ def test_long_contexts_whose_scores_move(S, shape, D, Hq):
     out = S.attn_prefill(cache, bf(q.reshape(n, -1)).cuda(), i32(cu), i32([kv]), i32(table), scale=1.0)
     ref, tol, written = A.attention(q.astype(np.float64), k, v, cu, [kv], table, scale=1.0)
     check(out, ref, tol, written, Hq, D)
+
+
+LONG_PREFIX = [
+    # batch, prefix, Hq, Hkv, D, page: repeated reads far above what makes the prefix's own pass pay
+    (40, 4096, 8, 4, 128, 64),
+    (70, 8192, 16, 2, 64, 256),    # 560 rows per key head: three tile pairs
+    (3, 32768, 14, 7, 128, 16),
+    (36, 4096, 96, 4, 128, 128),   # 24 query heads per key head
+]
+
+
+def long_prefix_case(S, B, prefix, Hq, Hkv, D, page, seed):
+    rng = np.random.default_rng(seed)
+    kv = [prefix + int(n) for n in rng.integers(0, 3 * page, size=B)]
+    kv[1 % B], kv[2 % B] = prefix, prefix + 1     # nothing of its own; one key
+    if B > 5:
+        kv[3], kv[4] = prefix - 100, 0            # ends inside the prefix; empty
+    table, n_pages = make_table(rng, kv, page, shared=prefix // page)
+    cache, k, v = make_cache(S, rng, kv, table, n_pages, Hkv, page, D)
+    q = bf(rng.normal(size=(B, Hq * D)) * 1.5)
+    return rng, kv, table, n_pages, cache, k, v, q
+
+
+@pytest.mark.parametrize("B,prefix,Hq,Hkv,D,page", LONG_PREFIX)
+def test_decode_long_prefix(S, B, prefix, Hq, Hkv, D, page):
+    rng, kv, table, n_pages, cache, k, v, q = long_prefix_case(S, B, prefix, Hq, Hkv, D, page, B + D)
+    ref, tol, written = A.attention(f64(q).reshape(B, Hq, D), k, v, range(B + 1), kv, table)
+    used = table.copy()
+    used[1:, :prefix // page] = -5  # only row 0 names the prefix's pages
+    ws = S.attn_decode_ws(cache, B, Hq, table.shape[1], prefix)
+    outs = []
+    for fill in (float("nan"), 1e30):
+        ws.view(torch.float32).fill_(fill)
+        outs.append(S.attn_decode(cache, q.cuda(), i32(kv), i32(used), prefix_len=prefix, ws=ws))
+        check(outs[-1], ref, tol, written, Hq, D)
+    assert torch.equal(*outs)
+    assert S.device_error() == 0
+    check(S.attn_decode(cache, q.cuda(), i32(kv), i32(table)), ref, tol, written, Hq, D)
+
+
+def test_decode_long_prefix_graph_and_invalid_pages(S):
+    B, prefix, Hq, Hkv, D, page = 40, 4096, 8, 4, 128, 64
+    rng, kv, table, n_pages, cache, k, v, q = long_prefix_case(S, B, prefix, Hq, Hkv, D, page, 71)
+    qd, lens, tab = q.cuda(), i32(kv), i32(table)
+    ws = S.attn_decode_ws(cache, B, Hq, table.shape[1], prefix)
+    out = torch.empty_like(qd)
+    S.attn_decode(cache, qd, lens, tab, prefix_len=prefix, O=out, ws=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        S.attn_decode(cache, qd, lens, tab, prefix_len=prefix, O=out, ws=ws)
+    shorter = [max(0, n - int(rng.integers(0, 80))) for n in kv]
+    for lengths in (kv, shorter, [0] * B, kv):
+        lens.copy_(i32(lengths))
+        out.fill_(7.0)
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+        ref, tol, written = A.attention(f64(q).reshape(B, Hq, D), k, v, range(B + 1), lengths, table)
+        check(out, ref, tol, written, Hq, D)
+    assert S.device_error() == 0
+    bad = table.copy()
+    bad[:, 7] = n_pages + 3
+    ref, tol, written = A.attention(f64(q).reshape(B, Hq, D), k, v, range(B + 1), kv, bad)
+    o = S.attn_decode(cache, qd, i32(kv), i32(bad), prefix_len=prefix)
+    assert S.device_error() == 5
+    check(o, ref, tol, written, Hq, D)

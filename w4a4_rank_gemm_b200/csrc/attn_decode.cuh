@@ -35,6 +35,7 @@ struct DecArgs {
   int n_heads, group, row_blocks;  // row_blocks: 16-head blocks per kv head
   int rows;     // rows per workspace slot, min(group, 16)
   int prefix;   // keys in front that the shared-prefix pass has done
+  int common;   // keys in front whose pages are sequence 0's
   int shares;   // G, two per CTA
   float* so;    // slots [2 G (+ batch x blocks of heads when prefix)][rows][D], normalised
   float* slse;  // [slot][rows]
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const int key = a.prefix + at.blk * kBlockKeys + lane * box;
       int pg = a.c_.n_pages;  // outside the map: filled with zeros
       if (lane < n * per_block && key < min(a.b.kv_len[at.b], cap)) {
-        const int e = a.b.table[(long long)at.b * a.b.ldt + (key >> a.c_.page_shift)];
+        const int e = a.b.table[(key < a.common ? 0 : (long long)at.b * a.b.ldt) + (key >> a.c_.page_shift)];
         if (e >= 0 && e < a.c_.n_pages) pg = e;
         else note_bad_page();
       }
