@@ -640,7 +640,10 @@ serq_status serq_mx_linear(const serq_mx_layer* q, const void* Xq, const void* x
  * count as zeros in attention (positions past the table are left out), and
  * serq_device_error reports 5.
  * Cached keys and values of positions below kv_len[b] have to be finite; what
- * lies behind them in a page, and other pages, may hold anything.
+ * lies behind them in a page, and other pages, may hold anything.  A NaN in a
+ * query, or in a key or value that a row sees, gives that row results that are
+ * not finite (one in a value also rows of the sequence in front of it), never
+ * another sequence's.
  * ---------------------------------------------------------------------------
  */
 typedef struct serq_rope serq_rope;

@@ -743,3 +743,86 @@ def test_decode_long_prefix_graph_and_invalid_pages(S):
     o = S.attn_decode(cache, qd, i32(kv), i32(bad), prefix_len=prefix)
     assert S.device_error() == 5
     check(o, ref, tol, written, Hq, D)
+
+
+NONFINITE = [  # q_lens, tokens before, Hq, Hkv, D, page
+    ([40, 300], [0, 0], 4, 4, 128, 32),      # whole items
+    ([64, 3], [4000, 900], 8, 2, 128, 16),   # cut ones, past 2048 keys
+    ([200, 5], [2300, 0], 2, 2, 64, 64),
+]
+
+
+@pytest.mark.parametrize("where", ["query", "key", "value"])
+@pytest.mark.parametrize("q_lens,past,Hq,Hkv,D,page", NONFINITE)
+def test_prefill_shows_nan(S, where, q_lens, past, Hq, Hkv, D, page):
+    """A NaN in a query, or in a key or value that a row sees, is in its result,
+    and nowhere in the other sequence's."""
+    rng = np.random.default_rng(81)
+    kv_lens = [a + b for a, b in zip(q_lens, past)]
+    cu = np.concatenate([[0], np.cumsum(q_lens)])
+    T = int(cu[-1])
+    table, n_pages = make_table(rng, kv_lens, page)
+    cache, k, v = make_cache(S, rng, kv_lens, table, n_pages, Hkv, page, D)
+    q = bf(rng.normal(size=(T, Hq * D)))
+    ref, tol, written = A.attention(f64(q).reshape(T, Hq, D), k, v, cu, kv_lens, table)
+    qd, group = q.cuda(), Hq // Hkv
+    for key in (past[0], past[0] + 1, past[0] + 6):
+        hit = np.zeros((T, Hq), bool)      # rows that have to show it
+        free = np.ones((T, Hq), bool)      # rows that may not
+        t = key - past[0]
+        if where == "query":
+            old = qd[t, D:2 * D].clone()
+            qd[t, D:2 * D] = float("nan")
+            hit[t, 1] = True
+            free = ~hit
+        else:
+            at = (cache.K if where == "key" else cache.V)[table[0, key // page], 0, key % page]
+            old = at.clone()
+            at[3] = float("nan")
+            hit[t:q_lens[0], :group] = True
+            free[(0 if where == "value" else t):q_lens[0], :group] = False
+        got = f64(S.attn_prefill(cache, qd, i32(cu), i32(kv_lens), i32(table))).reshape(T, Hq, D)
+        bad = ~np.isfinite(got)
+        assert np.all(bad[hit][:, 3] if where == "value" else bad[hit])
+        assert np.all(np.abs(got - ref)[free] <= tol[free])
+        if where == "query":
+            qd[t, D:2 * D] = old
+        else:
+            at.copy_(old)
+
+
+@pytest.mark.parametrize("where", ["query", "key", "value"])
+@pytest.mark.parametrize("kv_lens,prefix,Hq,Hkv,D,page", [
+    ([40, 64, 7000], 0, 4, 4, 128, 32),
+    ([300 + 11 * i for i in range(40)], 0, 8, 2, 64, 16),
+    ([4096 + 37 * i for i in range(40)], 4096, 8, 4, 128, 64),
+])
+def test_decode_shows_nan(S, where, kv_lens, prefix, Hq, Hkv, D, page):
+    rng = np.random.default_rng(82)
+    B = len(kv_lens)
+    table, n_pages = make_table(rng, kv_lens, page, shared=prefix // page)
+    cache, k, v = make_cache(S, rng, kv_lens, table, n_pages, Hkv, page, D)
+    q = bf(rng.normal(size=(B, Hq * D)))
+    ref, tol, written = A.attention(f64(q).reshape(B, Hq, D), k, v, range(B + 1), kv_lens, table)
+    qd, group = q.cuda(), Hq // Hkv
+    for b in (1, B - 1):
+        for key in {prefix, kv_lens[b] - 1} - {kv_lens[b]}:
+            hit = np.zeros((B, Hq), bool)
+            if where == "query":
+                old = qd[b, D:2 * D].clone()
+                qd[b, D:2 * D] = float("nan")
+                hit[b, 1] = True
+            else:
+                at = (cache.K if where == "key" else cache.V)[table[b, key // page], 0, key % page]
+                old = at.clone()
+                at[3] = float("nan")
+                hit[b, :group] = True
+            o = S.attn_decode(cache, qd, i32(kv_lens), i32(table), prefix_len=prefix)
+            got = f64(o).reshape(B, Hq, D)
+            bad = ~np.isfinite(got)
+            assert np.all(bad[hit][:, 3] if where == "value" else bad[hit])
+            assert np.all(np.abs(got - ref)[~hit] <= tol[~hit])
+            if where == "query":
+                qd[b, D:2 * D] = old
+            else:
+                at.copy_(old)

@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
               x.z += y.z;
               x.w += y.w;
             }
-            const float inv = z > 0.f ? 1.f / z : 0.f;
+            const float inv = z != 0.f ? 1.f / z : 0.f;  // a NaN stays one
             x.x *= inv;
             x.y *= inv;
             x.z *= inv;
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 float mm = -INFINITY;
 #pragma unroll
                 for (int v = 0; v < 4; ++v) mm = fmaxf(mm, st_m[v * 16 + row]);
-                a.slse[slot * a.rows + row] = z > 0.f ? mm + log2f(z) : -INFINITY;
+                a.slse[slot * a.rows + row] = z != 0.f ? mm + log2f(z) : -INFINITY;
               }
             }
           }
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(128) k_join(const DecArgs a) {
     float mx = lse;
 #pragma unroll
     for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    if (mx == -INFINITY) continue;
+    if (mx == -INFINITY && __all_sync(0xffffffffu, lse == -INFINITY)) continue;  // mx passes over a NaN
     const float mn = fmaxf(top, mx), f = ex2(top - mn);
     top = mn;
     const float w = lse == -INFINITY ? 0.f : ex2(lse - mn);
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(128) k_join(const DecArgs a) {
       for (int e = 0; e < E; ++e) acc[e] += f * all[v][lane * E + e];
     }
   }
-  const float inv = z > 0.f ? 1.f / z : 0.f;
+  const float inv = z != 0.f ? 1.f / z : 0.f;
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + b * a.ldo + (long long)h * D + lane * E);
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);

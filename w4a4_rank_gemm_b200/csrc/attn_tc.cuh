@@ -90,16 +90,24 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The larger one, or NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // 2^y on the FMA pipe: n = round(y), r = y - n in [-1/2, 1/2], a
 // degree-4 polynomial for 2^r (least maximum relative error with constant term
 // 1, found by reweighted least squares: 2.9e-6, a 1400th of the bf16 rounding that
 // follows), n added to its exponent.  -127 and below give 0; CAP: above 127 as
-// 127, else y stays below that.
+// 127, else y stays below that.  A NaN gives what is not finite as a bf16 (CAP:
+// 2^127, which is never used).
 template <bool CAP>
 __device__ __forceinline__ float2 ex2_fma(float2 y) {
   constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: the sum's low bits are n
-  y.x = fmaxf(y.x, -127.0f);
-  y.y = fmaxf(y.y, -127.0f);
+  y.x = max_nan(y.x, -127.0f);
+  y.y = max_nan(y.y, -127.0f);
   if (CAP) {
     y.x = fminf(y.x, 127.0f);
     y.y = fminf(y.y, 127.0f);
@@ -909,13 +917,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok) break;
         tc_fence_after();
       }
-      const float inv = l > 0.f ? 1.0f / l : 0.f;
+      const float inv = l != 0.f ? 1.0f / l : 0.f;  // a NaN stays one
       const int h = it.kvh * a.group + head;
       uint8_t* stage = smem + L::oStage + warp * 4096;
       if (it.slot >= 0) {
         const long long at = (long long)it.slot * 256 + 128 * x + row;
-        if (valid) a.plse[at] = l > 0.f ? mc + log2f(l) : -INFINITY;
-        const bool write = valid && l > 0.f;
+        if (valid) a.plse[at] = l != 0.f ? mc + log2f(l) : -INFINITY;
+        const bool write = valid && l != 0.f;
         const uint32_t writes = __ballot_sync(0xffffffffu, write);
         if (any) {
 #pragma unroll 1
@@ -964,8 +972,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               // a row that saw no key has inv = 0 and is written as zeros
-              const float v0 = l > 0.f ? __uint_as_float(o[e >> 2][(8 * e + 2 * k) & 31]) * inv : 0.f;
-              const float v1 = l > 0.f ? __uint_as_float(o[e >> 2][(8 * e + 2 * k + 1) & 31]) * inv : 0.f;
+              const float v0 = l != 0.f ? __uint_as_float(o[e >> 2][(8 * e + 2 * k) & 31]) * inv : 0.f;
+              const float v1 = l != 0.f ? __uint_as_float(o[e >> 2][(8 * e + 2 * k + 1) & 31]) * inv : 0.f;
               const __nv_bfloat162 b2 = __floats2bfloat162_rn(v0, v1);
               w[k] = reinterpret_cast<const uint32_t&>(b2);
             }
@@ -1138,7 +1146,7 @@ __global__ void __launch_bounds__(256, KP == 2 ? 2 : 1) k_merge(const TcArgs a) 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (at[i] < 0) continue;
-      const float inv = z[i] > 0.f ? 1.f / z[i] : 0.f;
+      const float inv = z[i] != 0.f ? 1.f / z[i] : 0.f;
       __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.o + at[i] + lane * E);
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) dst[e] = __floats2bfloat162_rn(acc[i][2 * e] * inv, acc[i][2 * e + 1] * inv);
