@@ -1,9 +1,10 @@
 // Decode attention: one query token per sequence over the paged cache, bound
 // by the bytes of K and V.
 //
-// Work is counted in blocks of 64 keys of one (sequence, kv head, 16 query
-// heads), laid end to end over the batch; share c of G is the c-th equal part,
-// whatever the lengths are, as the streaming GEMV shares the weights.  A share
+// Work is counted in units, laid end to end over the batch: a (sequence, kv
+// head, 16 query heads) pair's blocks of 64 keys and one more for its end, which
+// takes about as long as a block; share c of G is the c-th equal part, whatever
+// the lengths are, as the streaming GEMV shares the weights.  A share
 // is a run of segments: the end of one pair's keys, whole pairs, the beginning
 // of another's.  Whole pairs are finished here; the first and last segment of
 // a share may be partial and go to the workspace (slots 2c and 2c + 1), to be
@@ -67,6 +68,9 @@ __device__ __forceinline__ int dec_blocks(const DecArgs& a, int b) {
   return ceil_div(max(0, min(a.b.kv_len[b], cap) - a.prefix), kBlockKeys);
 }
 
+// Units of a pair of nb blocks.
+__device__ __forceinline__ int dec_units(int nb) { return nb + (nb > 0); }
+
 // Warp sum of non-negative counts; `small`: it stays below 2^31.
 __device__ __forceinline__ long long warp_sum(long long v, bool small) {
   if (small) return __reduce_add_sync(0xffffffffu, (uint32_t)v);
@@ -75,12 +79,12 @@ __device__ __forceinline__ long long warp_sum(long long v, bool small) {
   return v;
 }
 
-// Position in the batch's run of blocks.
+// Position in the batch's run of pairs.
 struct DecPos {
   int b, h, blk, nb;  // sequence, head block, next block, blocks of the sequence
 };
 
-// Finds a share's beginning.  Lane i counts the blocks of sequences
+// Finds a share's beginning.  Lane i counts the units of sequences
 // [i q, (i + 1) q), q = ceil(batch / 32), in one round of loads.
 struct DecFind {
   int q;
@@ -91,10 +95,10 @@ struct DecFind {
 #pragma unroll 4
     for (int i = 0; i < q; ++i) {
       const int b = lane * q + i;
-      if (b < a.b.batch) mine += dec_blocks(a, b);
+      if (b < a.b.batch) mine += dec_units(dec_blocks(a, b));
     }
     upto = mine;
-    if (a.b.batch <= 32) {  // fewer than 2^26 blocks each
+    if (a.b.batch <= 32) {  // fewer than 2^26 units each
       int v = (int)mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -112,7 +116,7 @@ struct DecFind {
       total = __shfl_sync(0xffffffffu, upto, 31);
     }
   }
-  // The place of block w < total * heads (the warp calls).
+  // The place of unit w < total * heads (the warp calls); blk = nb: a pair's end.
   __device__ DecPos find(const DecArgs& a, long long w, int heads) const {
     const int src = __ffs(__ballot_sync(0xffffffffu, w < upto * heads)) - 1;
     long long rest = w - __shfl_sync(0xffffffffu, upto - mine, src) * heads;
@@ -120,11 +124,11 @@ struct DecFind {
     p.b = src * q;
     for (;; ++p.b) {
       p.nb = dec_blocks(a, p.b);
-      if (rest < (long long)p.nb * heads) break;
-      rest -= (long long)p.nb * heads;
+      if (rest < (long long)dec_units(p.nb) * heads) break;
+      rest -= (long long)dec_units(p.nb) * heads;
     }
-    p.h = (int)quotient(rest, p.nb);
-    p.blk = (int)(rest - (long long)p.h * p.nb);
+    p.h = (int)quotient(rest, dec_units(p.nb));
+    p.blk = (int)(rest - (long long)p.h * dec_units(p.nb));
     return p;
   }
 };
@@ -197,14 +201,20 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   const int heads = a.c_.n_kv_heads * a.row_blocks;
   const DecFind batch(a, lane);
   const Shares shares(batch.total * heads, a.shares);
-  const long long w0 = share < a.shares ? shares.start(share) : 0;
+  long long w0 = share < a.shares ? shares.start(share) : 0;
   const long long w1 = share < a.shares ? shares.start(share + 1) : 0;
   const int cap = a.b.max_pages << a.c_.page_shift;
   // keys of a copy: a block's K or V lie in shared memory as box rows of its
   // first 64 columns, the same rows of the next 64, then the next box
   const int box = min(1 << a.c_.page_shift, kBlockKeys);
   DecPos p = {};
-  if (w0 < w1) p = batch.find(a, w0, heads);
+  if (w0 < w1) {
+    p = batch.find(a, w0, heads);
+    if (p.blk == p.nb) {  // another share has done the pair
+      dec_next_pair(a, p, heads);
+      ++w0;
+    }
+  }
 
   if (loads) {
     if (lane == 0) {
@@ -236,7 +246,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const int cur_n = n, cur_pg = pg;
       w += n;
       p.blk += n;
-      if (p.blk == p.nb) dec_next_pair(a, p, heads);
+      if (p.blk == p.nb) {
+        dec_next_pair(a, p, heads);
+        ++w;
+      }
       n = (int)min(min((long long)(p.nb - p.blk), w1 - w), (long long)max_n);
       if (w < w1) pg = lookup(p, n);
       const int y0 = ((cur.h / a.row_blocks) << a.c_.page_shift);
@@ -385,8 +398,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       }
       DecPos nx = p;  // the next segment, whose queries load during the join
       nx.blk = p.blk + n;
-      if (nx.blk == nx.nb) dec_next_pair(a, nx, heads);
-      if (w + n < w1) load_q(nx, qf);
+      w += n;
+      if (nx.blk == nx.nb) {
+        dec_next_pair(a, nx, heads);
+        ++w;
+      }
+      if (w < w1) load_q(nx, qf);
       // ------------------------------------------------- join the four warps
 #pragma unroll
       for (int d = 1; d < 4; d <<= 1) {
@@ -471,7 +488,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       };
       if (nrows <= 8) join(std::integral_constant<int, 8>{});
       else join(std::integral_constant<int, 16>{});
-      w += n;
       p = nx;
     }
   }
@@ -502,7 +518,7 @@ __global__ void __launch_bounds__(128) k_join(const DecArgs a) {
   const int heads = a.c_.n_kv_heads * a.row_blocks;
   long long before = 0, total = 0;
   for (int i = lane; i < a.b.batch; i += 32) {
-    const int n = dec_blocks(a, i);
+    const int n = dec_units(dec_blocks(a, i));
     total += n;
     if (i < b) before += n;
   }
@@ -511,7 +527,7 @@ __global__ void __launch_bounds__(128) k_join(const DecArgs a) {
   const int kvh = h / a.group, hr = h - kvh * a.group;
   const int hb = kvh * a.row_blocks + hr / 16, row = hr & 15;
   const int nb = dec_blocks(a, b);
-  const long long s0 = before * heads + (long long)hb * nb, s1 = s0 + nb;
+  const long long s0 = before * heads + (long long)hb * dec_units(nb), s1 = s0 + nb;
   // shares that hold the pair's first and last block
   const Shares shares(total, a.shares);
   int c0 = 0, c1 = -1;
