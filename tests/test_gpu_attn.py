@@ -826,3 +826,21 @@ def test_decode_shows_nan(S, where, kv_lens, prefix, Hq, Hkv, D, page):
                 qd[b, D:2 * D] = old
             else:
                 at.copy_(old)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(4, 4, 128, 64), (40, 2, 64, 16)])
+def test_decode_cuts_at_every_block(S, Hq, Hkv, D, page):
+    """Lengths of 0 to a few blocks beside long ones: shares begin inside a
+    pair, at its first block and behind its last one."""
+    rng = np.random.default_rng(91)
+    for lens in ([1] * 200, list(range(60, 70)) * 9, [0, 64, 0, 128, 1] * 12 + [4000],
+                 [int(n) for n in rng.integers(0, 400, size=77)], [20000, 1, 1], [193]):
+        table, n_pages = make_table(rng, lens, page)
+        cache, k, v = make_cache(S, rng, lens, table, n_pages, Hkv, page, D)
+        B = len(lens)
+        q = bf(rng.normal(size=(B, Hq * D)))
+        ref, tol, written = A.attention(f64(q).reshape(B, Hq, D), k, v, range(B + 1), lens, table)
+        ws = S.attn_decode_ws(cache, B, Hq, table.shape[1])
+        ws.view(torch.float32).fill_(float("nan"))
+        check(S.attn_decode(cache, q.cuda(), i32(lens), i32(table), ws=ws), ref, tol, written, Hq, D)
+    assert S.device_error() == 0
