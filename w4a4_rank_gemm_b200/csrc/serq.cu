@@ -2062,9 +2062,9 @@ int pair_shift(int tokens) {
 // prompts make them uneven.  Equal shares let idle SMs take part, at the price of
 // writing, reading and joining the cut items' parts.  They are taken when the
 // steps saved (of 128 keys; about 1.8 us) pay for that: 32 items of 48 steps
-// (40 tokens over 6000) 39 us, whole 78; 104 of up to 60 steps 79, whole 100; 32 of
-// 14 steps 22.6, whole 30.2; but 96 of 28 steps 68, whole 60; 128 of 35 steps 95,
-// whole 75; 19 of 5 steps 23.5, whole 16.6.
+// (40 tokens over 6000) 39 us, whole 78; 104 of up to 60 steps 76, whole 99; 32 of
+// 14 steps 22.6, whole 30.2; 96 of 18 to 41 steps 56, whole 70; but 96 of 28 steps
+// 65, whole 61; 128 of 35 steps 95, whole 75; 19 of 5 steps 21, whole 16.6.
 struct PrefillPlan {
   int group, tokens, shares, ctas;
   bool longer;  // items of more than 16 steps: see k_attn's LONG
@@ -2081,7 +2081,7 @@ PrefillPlan prefill_plan(const serq_kv_cache* c, int T, int n_heads, int batch, 
   const long long keys = max_kv ? std::min<long long>(max_kv, cap) : cap;
   // (items is a bound: a little above one per SM it may well be one)
   const long long rounds = items * 7 < sms * 8 ? 1 : 2, saved = keys * (rounds * sms - items) / (128 * sms);
-  const bool share = items < 2 * sms && saved >= 5 + items / 10 && (rounds == 1 || keys * batch >= 3ll * T);
+  const bool share = items < 2 * sms && saved >= 5 + items / 16 && (rounds == 1 || keys * batch >= 3ll * T);
   p.shares = share ? serq::attn::tc_shares(items, keys, (int)sms) : 0;
   p.longer = keys > 2048;
   p.ctas = share ? p.shares : (int)std::min(items, sms);
