@@ -759,7 +759,7 @@ serq_status serq_attn_prefill(const serq_kv_cache* cache, const void* Q, int ldq
  *              prefix_len positions of every sequence are the same tokens, in
  *              the pages of page_table row 0; entries of other rows below
  *              prefix_len / page_size are not used.  They are read once for the
- *              whole batch, unless too little is saved by that (below 112 MB of
+ *              whole batch, unless too little is saved by that (below 128 MB of
  *              repeated reads).  kv_len[b] < prefix_len cuts sequence b's part.
  *  max_kv, ws  as above, with serq_attn_decode_ws_bytes.
  */

@@ -2165,10 +2165,11 @@ DecodePlan decode_plan(const serq_kv_cache* c, int batch, int n_heads, int max_p
   // A shared prefix has its own pass when reading it once for the batch saves
   // more than that pass costs, else every sequence reads it (from the pages of
   // row 0 all the same, so mostly from L2).  With the pass and without: 24 MB
-  // saved (4 sequences, 2048 shared, 8 kv heads) 14.9 and 11.9 us, 96 MB 24.1 and
-  // 20.1, 112 MB (8 sequences, 4096 shared) 17.5 and 20.3, 448 MB 31.4 and 53.3.
+  // saved (4 sequences, 2048 shared, 8 kv heads) 14.8 and 11.3 us, 96 MB 22.7 and
+  // 19.4, 120 MB (16 sequences, 2048 shared) 22.8 and 21.8, 240 MB (16 sequences,
+  // 1024 shared, 32 kv heads) 32.3 and 38.6, 448 MB 27.7 and 50.9.
   const long long saved = (batch - 1ll) * prefix_len * c->n_kv_heads * c->head_dim * 4;
-  p.prefix = saved >= (112ll << 20) ? prefix_len : 0;
+  p.prefix = saved >= (128ll << 20) ? prefix_len : 0;
   const long long cap = (long long)max_pages * c->page_size;
   const long long keys = std::max(0ll, (max_kv ? std::min<long long>(max_kv, cap) : cap) - p.prefix);
   const long long blocks = (keys + serq::attn::kBlockKeys - 1) / serq::attn::kBlockKeys * batch * c->n_kv_heads * p.row_blocks;
