@@ -14,12 +14,12 @@
 // joined in share order by k_join.
 //
 // A CTA works on two shares at once, so that one's joining of warps at a
-// segment's end (about 2000 cycles) overlaps the other's blocks.  Each has four
+// segment's end (about 1400 cycles) overlaps the other's blocks.  Each has four
 // warps, 16 keys of a block each, and a warp that streams K and V blocks by TMA
 // into its ring (192 KB in flight per SM), across segment boundaries.  Scores
-// and output by mma.sync m16n8k16 with the group's query heads as the 16 rows.  Their use of the tensor core is far below its
-// rate (16 flop per byte read), so nothing is gained by tcgen05 here; its
-// 128-row tiles would be 1/32 to 1/8 full.
+// and output by mma.sync m16n8k16 with the group's query heads as the 16 rows.
+// Their use of the tensor core is far below its rate (16 flop per byte read), so
+// nothing is gained by tcgen05 here; its 128-row tiles would be 1/32 to 1/8 full.
 #pragma once
 
 #include "attn_tc.cuh"
@@ -671,8 +671,8 @@ inline cudaError_t launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV,
   e = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, a);
   if (e != cudaSuccess) return e;
   // Four warps share a head's parts when there are few heads, and so many parts
-  // of each (one sequence of 8191 keys, 32 heads in 37 parts: 14.3 us with four,
-  // 22.8 with one; 64 sequences over a prefix: 64.8 with four, 60.4 with one).
+  // of each (one sequence of 8191 keys, 32 heads in 37 parts: 11.7 us with four,
+  // 15.4 with one; 64 sequences over a prefix: 60.8 with four, 51.7 with one).
   const bool few = (long long)a.b.batch * a.n_heads <= 512;
   cfg.gridDim = dim3(a.b.batch, few ? a.n_heads : (a.n_heads + 3) / 4);
   cfg.blockDim = dim3(128);
