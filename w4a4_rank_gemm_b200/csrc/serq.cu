@@ -130,6 +130,14 @@ bool make_map_bf16_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Pageable host memory to the device, complete on return.  (cudaMemcpy alone
+// returns once the source is staged: the copy itself is ordered with the legacy
+// default stream, but not with streams that do not wait for that one.)
+cudaError_t upload(void* dst, const void* src, size_t bytes) {
+  const cudaError_t e = cudaMemcpy(dst, src, bytes, cudaMemcpyHostToDevice);
+  return e == cudaSuccess ? cudaStreamSynchronize(cudaStreamLegacy) : e;
+}
+
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
@@ -1060,8 +1068,8 @@ struct Uploads {
       return fail(SERQ_ERR_ALLOC, "cudaMalloc(%zu) for an upload failed: %s", count * sizeof(T), cudaGetErrorString(e));
     }
     bufs.push_back(d);
-    e = cudaMemcpy(d, host, count * sizeof(T), cudaMemcpyHostToDevice);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy of a prepare input");
+    e = upload(d, host, count * sizeof(T));
+    if (e != cudaSuccess) return cuda_fail(e, "upload of a prepare input");
     *out = static_cast<const T*>(d);
     return SERQ_OK;
   }
@@ -1904,7 +1912,7 @@ serq_status serq_rope_create(const serq_rope_opts* o, serq_rope** out) {
     cudaGetLastError();
     return fail(SERQ_ERR_ALLOC, "cudaMalloc failed: %s", cudaGetErrorString(e));
   }
-  e = cudaMemcpy(r->turns, turns, half * sizeof(double), cudaMemcpyHostToDevice);
+  e = upload(r->turns, turns, half * sizeof(double));
   if (e != cudaSuccess) {
     cudaFree(r->turns);
     delete r;
