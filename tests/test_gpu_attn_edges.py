@@ -35,3 +35,34 @@ def test_rotation_is_ready_on_any_stream(S, D, rot, layout):
         y, mag = A.rotate(f64(k).reshape(T, Hkv, D), np.arange(T), A.frequencies(rot, theta), layout)
         assert np.all(np.abs(keys - y) <= A.rotate_bound(y, mag, False))
     assert S.device_error() == 0
+
+
+def test_calls_behind_a_long_one(S):
+    """A call whose blocks start beside a kernel that lasts longer than the
+    bounded waits' second: its waits do not count that kernel's time."""
+    rng = np.random.default_rng(102)
+    D, page, far = 128, 256, 1 << 27
+    # one row over 2^27 keys, the same page again and again, on one SM (a hint of one key: no shares)
+    K = bf(rng.normal(size=(1, 1, page, D))).cuda()
+    one = S.KVCache(K=K, V=K.clone())
+    table = torch.zeros((1, far // page), dtype=torch.int32, device="cuda")
+    q1 = bf(rng.normal(size=(1, D))).cuda()
+    kv, Hq, Hkv = [900, 70], 8, 2
+    tab, n_pages = make_table(rng, kv, 64)
+    cache, k, v = make_cache(S, rng, kv, tab, n_pages, Hkv, 64, D)
+    q = bf(rng.normal(size=(2, Hq * D)))
+    qd, lens, tabd, cu = q.cuda(), i32(kv), i32(tab), i32([0, 1, 2])
+    ref, tol, written = A.attention(f64(q).reshape(2, Hq, D), k, v, [0, 1, 2], kv, tab)
+    far_len, far_cu = i32([far]), i32([0, 1])
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    torch.cuda.synchronize()
+    e0.record()
+    S.attn_prefill(one, q1, far_cu, far_len, table, max_kv=1)
+    o = S.attn_prefill(cache, qd, cu, lens, tabd)
+    p = S.attn_decode(cache, qd, lens, tabd)
+    e1.record()
+    torch.cuda.synchronize()
+    assert e0.elapsed_time(e1) > 1050.0, "the first kernel ended within the waits' limit: nothing is tested"
+    assert S.device_error() == 0
+    check(o, ref, tol, written, Hq, D)
+    check(p, ref, tol, written, Hq, D)

@@ -17,6 +17,8 @@
 //
 // Warps: 0-3 softmax of A (one row per thread), 4-7 of B, 8 loads, 9 MMAs, 10
 // zeroes values behind the last key, 11 decodes work items ahead.
+// Every role waits for the grid in front before its first bounded wait, whose
+// limit then never counts that grid's time.
 // Persistent: a CTA takes work items (tile pair, kv head, range of key steps)
 // and the next item's Q, K and first scores overlap the epilogue of the last.
 #pragma once
@@ -503,6 +505,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
       }
+      grid_dep_wait();
       const int page = 1 << a.c_.page_shift;
       const int box = min(page, kTileKeys);         // rows per copy
       const int copies = kTileKeys / box * L::kHalves;  // per step and operand
@@ -572,6 +575,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // between them on waits and votes leaves the tensor core idle (with the
       // whole warp waiting and electing a lane each time, a step of two tiles
       // took 3400 cycles, 2048 of them MMAs).
+      grid_dep_wait();
       if (elect_one()) {
         const uint32_t idesc_qk = umma_idesc_bf16(128, kTileKeys, false, a.neg);
         constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D, true, false);
@@ -706,6 +710,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // anything, and a zero weight times a NaN is one: on the MMA thread's
       // request they are zeroed once they have landed.
       constexpr int kHalfBytes = L::kTile / L::kHalves;
+      grid_dep_wait();
       for (uint32_t n = 0;; ++n) {
         // lasts as long as the kernel does: the MMA thread, whose own waits are
         // bounded, always ends it
@@ -756,6 +761,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ------------------------------------------------------------- softmax
+    grid_dep_wait();
     const int x = warp >> 2;
     const int row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
