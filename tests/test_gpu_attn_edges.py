@@ -66,3 +66,57 @@ def test_calls_behind_a_long_one(S):
     assert S.device_error() == 0
     check(o, ref, tol, written, Hq, D)
     check(p, ref, tol, written, Hq, D)
+
+
+def has_own_pass(S, cache, B, Hq, cols, prefix):
+    ws = [S._ws_bytes(cache, S.lib.serq_attn_decode_ws_bytes, B, Hq, cols, p, 0) for p in (0, prefix)]
+    return ws[0] != ws[1]
+
+
+# ----------------------------------------------------- what is not finite, and large
+def cliff_cache(rng, kv, page, D, edge, nan_at):
+    """One kv head: keys of score 0 up to `edge`, of 500 from there on (for a
+    query of e_0 and a scale of 1), and a NaN key far in front."""
+    table, n_pages = make_table(rng, [kv], page)
+    k = np.zeros((n_pages, 1, page, D), np.float32)
+    v = rng.normal(size=k.shape).astype(np.float32)
+    for j in range(edge, kv):
+        k[table[0, j // page], 0, j % page, 0] = 500.0
+    for j in nan_at:
+        k[table[0, j // page], 0, j % page, 3] = np.nan
+    return table, k, v
+
+
+@pytest.mark.parametrize("D,Hq,kv,rows", [(128, 1, 4000, 1), (64, 4, 2000, 20), (128, 1, 900, 300)])
+def test_prefill_shows_nan_beside_much_larger_scores(S, D, Hq, kv, rows):
+    """A NaN key whose part of the row, or whose step, weighs nothing beside a
+    later one still shows, wherever in a step it lies."""
+    page = 64
+    for at in (0, 1, 2, 7, 8, 9, 64, 127, 130):
+        rng = np.random.default_rng(106)
+        table, k, v = cliff_cache(rng, kv, page, D, kv - rows - 60, [at])
+        cache = S.KVCache(K=bf(k).cuda(), V=bf(v).cuda())
+        q = np.zeros((rows, Hq, D), np.float32)
+        q[:, :, 0] = 1.0
+        for hint in (0, 1):  # cut into shares where few items are long, and whole
+            o = S.attn_prefill(cache, bf(q.reshape(rows, -1)).cuda(), i32([0, rows]), i32([kv]), i32(table), scale=1.0,
+                               max_kv=hint)
+            assert not torch.isfinite(o.float()).any(), (at, hint)
+
+
+def test_decode_shows_nan_beside_much_larger_scores(S):
+    B, prefix, Hq, Hkv, D, page = 70, 8192, 2, 1, 128, 64
+    for at in (0, 1, 5, 8192 - 16, 8192 - 1):
+        rng = np.random.default_rng(107)
+        kv = prefix + 100
+        table, k, v = cliff_cache(rng, kv, page, D, prefix + 10, [at])
+        full = np.repeat(table, B, 0)
+        full[:, prefix // page:] = table[0, prefix // page:]
+        cache = S.KVCache(K=bf(k).cuda(), V=bf(v).cuda())
+        assert has_own_pass(S, cache, B, Hq, full.shape[1], prefix)
+        q = np.zeros((B, Hq, D), np.float32)
+        q[:, :, 0] = 1.0
+        lens = i32([kv] * B)
+        for p in (0, prefix):
+            o = S.attn_decode(cache, bf(q.reshape(B, -1)).cuda(), lens, i32(full), prefix_len=p, scale=1.0)
+            assert not torch.isfinite(o.float()).any(), (at, p)

@@ -125,9 +125,9 @@ __device__ __forceinline__ float2 ex2_fma(float2 y) {
                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
@@ -857,11 +857,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           mask(r[1], c0 + 32);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            mx0 = max3(mx0, __uint_as_float(r[0][e]), __uint_as_float(r[0][e + 1]));
-            mx1 = max3(mx1, __uint_as_float(r[1][e]), __uint_as_float(r[1][e + 1]));
+            mx0 = max3_nan(mx0, __uint_as_float(r[0][e]), __uint_as_float(r[0][e + 1]));
+            mx1 = max3_nan(mx1, __uint_as_float(r[1][e]), __uint_as_float(r[1][e + 1]));
           }
         }
-        const float cand = fmaxf(mx0, mx1) * a.c;
+        const float cand = max_nan(mx0, mx1) * a.c;
+        // A NaN score makes the row's sum one, and so its result and its log-sum,
+        // whatever weight its part has in the end; exponentials on the FMA pipe
+        // turn it into 2^127 at most, which a larger score would outweigh.
+        if (cand != cand) l = cand;
         // the maximum in use follows only when it falls behind by 2^8: weights
         // up to 2^8 cost nothing in bf16 or fp32, and most steps leave O alone
         const bool grow = valid && cand > mc + kLazyMax;
