@@ -68,6 +68,15 @@ def test_calls_behind_a_long_one(S):
     check(p, ref, tol, written, Hq, D)
 
 
+def prefix_case(rng, kv, prefix, page, Hkv, D):
+    """Table whose row 0 names every page of the prefix that any sequence uses."""
+    table, n_pages = make_table(rng, kv, page, shared=prefix // page)
+    far = int(np.argmax(kv))
+    n = min(prefix // page, -(-kv[far] // page))
+    table[0, :n] = table[far, :n]
+    return table, n_pages
+
+
 def has_own_pass(S, cache, B, Hq, cols, prefix):
     ws = [S._ws_bytes(cache, S.lib.serq_attn_decode_ws_bytes, B, Hq, cols, p, 0) for p in (0, prefix)]
     return ws[0] != ws[1]
@@ -120,3 +129,20 @@ def test_decode_shows_nan_beside_much_larger_scores(S):
         for p in (0, prefix):
             o = S.attn_decode(cache, bf(q.reshape(B, -1)).cuda(), lens, i32(full), prefix_len=p, scale=1.0)
             assert not torch.isfinite(o.float()).any(), (at, p)
+
+
+def test_sequences_longer_than_a_table_of_prefix_only(S):
+    """A table that holds the prefix and nothing else: what it holds is attended
+    to, and lengths beyond it are reported."""
+    rng = np.random.default_rng(104)
+    B, prefix, Hq, Hkv, D, page = 20, 8192, 8, 2, 128, 64
+    kv = [prefix] * B
+    table, n_pages = prefix_case(rng, kv, prefix, page, Hkv, D)
+    cache, k, v = make_cache(S, rng, kv, table, n_pages, Hkv, page, D)
+    assert has_own_pass(S, cache, B, Hq, table.shape[1], prefix)
+    q = bf(rng.normal(size=(B, Hq * D)))
+    ref, tol, written = A.attention(f64(q).reshape(B, Hq, D), k, v, range(B + 1), kv, table)
+    for lens, code in ((kv, 0), ([prefix + 1] + kv[1:], 5), (kv[1:] + [prefix + 700], 5)):
+        o = S.attn_decode(cache, q.cuda(), i32(lens), i32(table), prefix_len=prefix)
+        assert S.device_error() == code
+        check(o, ref, tol, written, Hq, D)

@@ -301,9 +301,16 @@ __device__ __forceinline__ Measure measure(const TcArgs& a, const Pairs& s) {
 }
 
 // The one pseudo-sequence of a decode batch's shared prefix (the warp calls).
+// Where the table holds nothing but the prefix no other kernel sees a sequence
+// that is longer than it.
 __device__ __forceinline__ Pairs prefix_pairs(const TcArgs& a, int lane) {
+  const int cap = a.b.max_pages << a.c_.page_shift;
   int m = 0;
-  for (int b = lane; b < a.b.batch; b += 32) m = max(m, min(a.b.kv_len[b], a.prefix));
+  for (int b = lane; b < a.b.batch; b += 32) {
+    const int kv = a.b.kv_len[b];
+    m = max(m, min(kv, a.prefix));
+    if (kv > cap) note_bad_page();
+  }
   Pairs s;
   s.n = a.T;
   s.first = 0;
