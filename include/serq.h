@@ -631,7 +631,8 @@ serq_status serq_mx_linear(const serq_mx_layer* q, const void* Xq, const void* x
  *              kv_len[b] - (cu_q[b+1] - t); a row whose position is negative
  *              belongs to no token: serq_rope_append leaves it alone,
  *              attention writes zeros.
- *  page_table  batch rows of max_pages page indices, row stride ld_table;
+ *  page_table  batch rows of max_pages page indices, row stride ld_table,
+ *              max_pages page_size <= 2^31 - 128;
  *              position p of sequence b lies in page
  *              page_table[b][p / page_size], slot p % page_size.  Only the
  *              entries of positions below kv_len[b] are used.

@@ -146,3 +146,23 @@ def test_sequences_longer_than_a_table_of_prefix_only(S):
         o = S.attn_decode(cache, q.cuda(), i32(lens), i32(table), prefix_len=prefix)
         assert S.device_error() == code
         check(o, ref, tol, written, Hq, D)
+
+
+def test_tables_of_more_positions_than_32_bits_round(S):
+    """2^31 - 16 positions: the last blocks of keys would end behind 2^31."""
+    D, page = 128, 16
+    cache, rope = S.KVCache(8, page, 2, D), S.Rope(D)
+    q = torch.zeros((1, 4 * D), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 5.0)
+    cu, kv, tab = i32([0, 1]), i32([1]), i32([[0]])
+    L, p, cols = S.lib, S._ptr, (1 << 27) - 1
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    assert L.serq_rope_append(rope.handle, cache.handle, p(q), 4 * D, p(q), 4 * D, p(q), 4 * D, 1, 4, None, None, 0.0, 1,
+                              p(cu), p(kv), p(tab), cols, cols, p(out), 4 * D, None) == S.ERR_INVALID_ARG
+    assert L.serq_attn_prefill(cache.handle, p(q), 4 * D, 1, 4, 1.0, 1, p(cu), p(kv), p(tab), cols, cols, 0, p(ws),
+                               ws.numel(), p(out), 4 * D, None) == S.ERR_INVALID_ARG
+    assert L.serq_attn_decode(cache.handle, p(q), 4 * D, 4, 1.0, 1, p(kv), p(tab), cols, cols, 0, 0, p(ws), ws.numel(),
+                              p(out), 4 * D, None) == S.ERR_INVALID_ARG
+    assert b"max_pages" in L.serq_last_error_string()
+    torch.cuda.synchronize()
+    assert bool((out == 5.0).all())

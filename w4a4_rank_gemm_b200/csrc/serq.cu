@@ -1831,7 +1831,8 @@ serq_status check_batch(const serq_kv_cache* c, int batch, const int32_t* kv_len
                         int ld_table) {
   if (!kv_len || !table) return fail(SERQ_ERR_INVALID_ARG, "null kv_len or page_table");
   if (batch < 1) return fail(SERQ_ERR_INVALID_ARG, "batch = %d out of range", batch);
-  if (max_pages < 1 || (int64_t)max_pages * c->page_size > 0x7fffffff)
+  // (kernels round a number of keys up to 128, in 32 bits)
+  if (max_pages < 1 || (int64_t)max_pages * c->page_size > 0x7fffff80)
     return fail(SERQ_ERR_INVALID_ARG, "max_pages = %d out of range", max_pages);
   if (ld_table < max_pages) return fail(SERQ_ERR_INVALID_ARG, "ld_table (%d) < max_pages (%d)", ld_table, max_pages);
   return SERQ_OK;
