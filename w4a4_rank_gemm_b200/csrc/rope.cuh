@@ -15,7 +15,7 @@
 // of HBM time for 2048 tokens of 96 heads of 128.
 #pragma once
 
-#include "common.cuh"
+#include "attn_common.cuh"
 
 namespace serq {
 
