@@ -517,8 +517,11 @@ template <int D, int W>
 __global__ void __launch_bounds__(128) k_join(const DecArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
   const int h = min((int)blockIdx.y * (4 / W) + warp / W, a.n_heads - 1), mine = warp % W;
-  // the lengths are inputs of the call: k_decode_attn lets this grid start
-  // only after its own wait, so they are complete here
+  // The lengths are inputs of the call: k_decode_attn lets this grid start
+  // only after its own wait (or starts behind a prefix pass that has waited), so
+  // they were complete before this grid was launched.  (Read past L1 they would
+  // not depend on a launch finding L1 clean, at 100 sequences of 1 ... 60 keys
+  // 43.2 us for 33.8, one of 8191 13.9 for 11.7.)
   const int heads = a.c_.n_kv_heads * a.row_blocks;
   long long before = 0, total = 0;
   for (int i = lane; i < a.b.batch; i += 32) {
