@@ -131,6 +131,65 @@ def test_decode_shows_nan_beside_much_larger_scores(S):
             assert not torch.isfinite(o.float()).any(), (at, p)
 
 
+PREFIX_ENDS = [
+    # batch, prefix, longest past it (negative: inside it), Hq, Hkv, D, page
+    (40, 4112, 100, 8, 4, 128, 16),     # 16 keys in the last step of 128
+    (33, 4000, 70, 6, 6, 64, 32),       # 32
+    (20, 8256, 200, 14, 2, 128, 64),    # 64
+    (6, 2160, 40, 60, 60, 64, 16),      # 112, and shares that begin and end inside them
+    (24, 8192, -1191, 8, 2, 128, 64),   # the longest sequence ends inside the prefix, and inside a page
+    (70, 2048, -1, 4, 4, 64, 256),
+    (3, 33040, 1, 7, 7, 128, 16),
+]
+
+
+@pytest.mark.parametrize("B,prefix,past,Hq,Hkv,D,page", PREFIX_ENDS)
+def test_prefix_pass_ends(S, B, prefix, past, Hq, Hkv, D, page):
+    """Prefixes that end inside a step, lengths that end inside the prefix; NaN
+    behind every sequence's last key."""
+    rng = np.random.default_rng(prefix + B)
+    top = prefix + past
+    kv = [top - int(n) for n in rng.integers(0, max(1, abs(past)) + 300, size=B)]
+    kv[B // 2] = top
+    kv[0] = 5
+    if B > 3:
+        kv[1] = 0
+    table, n_pages = prefix_case(rng, kv, prefix, page, Hkv, D)
+    cache, k, v = make_cache(S, rng, kv, table, n_pages, Hkv, page, D)
+    if table.shape[1] * page < prefix:  # the table holds the whole prefix, whatever the lengths
+        wide = np.full((B, prefix // page), -7, np.int64)
+        wide[:, :table.shape[1]] = table
+        table = wide
+    assert has_own_pass(S, cache, B, Hq, table.shape[1], prefix)
+    q = bf(rng.normal(size=(B, Hq * D)) * 1.5)
+    full = table.copy()
+    full[:, :prefix // page] = table[0, :prefix // page]
+    ref, tol, written = A.attention(f64(q).reshape(B, Hq, D), k, v, range(B + 1), kv, full)
+    used = table.copy()
+    used[1:, :prefix // page] = -5
+    ws = S.attn_decode_ws(cache, B, Hq, table.shape[1], prefix)
+    for fill in (float("nan"), 1e30):
+        ws.view(torch.float32).fill_(fill)
+        check(S.attn_decode(cache, q.cuda(), i32(kv), i32(used), prefix_len=prefix, ws=ws), ref, tol, written, Hq, D)
+    assert S.device_error() == 0
+
+
+@pytest.mark.parametrize("prefix", [0, 4096 + 48])
+@pytest.mark.parametrize("scale,spread", [(0.0, 1.0), (-0.2, 1.0), (1.0, 4.0), (-1.0, 4.0), (1e-3, 1.0)])
+def test_decode_scales(S, scale, spread, prefix):
+    """No scale, negative ones and logits of several hundred, with the prefix's
+    own pass and without."""
+    rng = np.random.default_rng(103)
+    Hq, Hkv, D, page, B = 16, 4, 128, 16, 20
+    kv = [prefix + int(n) for n in rng.integers(1, 300, size=B)]
+    table, n_pages = prefix_case(rng, kv, prefix, page, Hkv, D)
+    cache, k, v = make_cache(S, rng, kv, table, n_pages, Hkv, page, D, spread=spread)
+    assert has_own_pass(S, cache, B, Hq, table.shape[1], prefix) == (prefix > 0)
+    q = bf(rng.normal(size=(B, Hq * D)))
+    ref, tol, written = A.attention(f64(q).reshape(B, Hq, D), k, v, range(B + 1), kv, table, scale=scale)
+    check(S.attn_decode(cache, q.cuda(), i32(kv), i32(table), prefix_len=prefix, scale=scale), ref, tol, written, Hq, D)
+
+
 def test_sequences_longer_than_a_table_of_prefix_only(S):
     """A table that holds the prefix and nothing else: what it holds is attended
     to, and lengths beyond it are reported."""
@@ -166,3 +225,32 @@ def test_tables_of_more_positions_than_32_bits_round(S):
     assert b"max_pages" in L.serq_last_error_string()
     torch.cuda.synchronize()
     assert bool((out == 5.0).all())
+
+
+# ------------------------------------------------------------------ wide tables
+@pytest.mark.parametrize("q_lens,past,Hq,Hkv,D,page", [
+    ([33], [0], 8, 2, 128, 64),
+    ([512], [0], 8, 2, 64, 16),
+    ([700, 1, 90], [0, 2500, 33], 4, 4, 128, 128),
+])
+def test_tables_wider_than_the_sequences(S, q_lens, past, Hq, Hkv, D, page):
+    """Tables as wide as a context limit, their unused entries invalid: the
+    split differs, results do not."""
+    rng = np.random.default_rng(105)
+    kv = [a + b for a, b in zip(q_lens, past)]
+    cu = np.concatenate([[0], np.cumsum(q_lens)])
+    T, B = int(cu[-1]), len(kv)
+    table, n_pages = make_table(rng, kv, page)
+    cache, k, v = make_cache(S, rng, kv, table, n_pages, Hkv, page, D)
+    q, qd = bf(rng.normal(size=(T, Hq * D))), bf(rng.normal(size=(B, Hq * D)))
+    ref, tol, written = A.attention(f64(q).reshape(T, Hq, D), k, v, cu, kv, table)
+    dref, dtol, dwritten = A.attention(f64(qd).reshape(B, Hq, D), k, v, range(B + 1), kv, table)
+    for limit in (4096, 32768, 131072):
+        wide = np.full((B, limit // page), -9, np.int64)
+        wide[:, :table.shape[1]] = table
+        for hint in (0, max(kv)):
+            o = S.attn_prefill(cache, q.cuda(), i32(cu), i32(kv), i32(wide), max_kv=hint)
+            check(o, ref, tol, written, Hq, D)
+            o = S.attn_decode(cache, qd.cuda(), i32(kv), i32(wide), max_kv=hint)
+            check(o, dref, dtol, dwritten, Hq, D)
+    assert S.device_error() == 0
