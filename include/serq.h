@@ -760,8 +760,9 @@ serq_status serq_attn_prefill(const serq_kv_cache* cache, const void* Q, int ldq
  *              prefix_len positions of every sequence are the same tokens, in
  *              the pages of page_table row 0; entries of other rows below
  *              prefix_len / page_size are not used.  They are read once for the
- *              whole batch, unless too little is saved by that (below 128 MB of
- *              repeated reads).  kv_len[b] < prefix_len cuts sequence b's part.
+ *              whole batch, unless reading them again costs less than that (few
+ *              sequences or a short prefix).  kv_len[b] < prefix_len cuts
+ *              sequence b's part.
  *  max_kv, ws  as above, with serq_attn_decode_ws_bytes.
  */
 size_t serq_attn_decode_ws_bytes(const serq_kv_cache* cache, int batch, int n_heads, int max_pages, int prefix_len,

@@ -2172,13 +2172,30 @@ DecodePlan decode_plan(const serq_kv_cache* c, int batch, int n_heads, int max_p
   p.row_blocks = (p.group + 15) / 16;
   p.rows = std::min(p.group, 16);
   // A shared prefix has its own pass when reading it once for the batch saves
-  // more than that pass costs, else every sequence reads it (from the pages of
-  // row 0 all the same, so mostly from L2).  With the pass and without: 24 MB
-  // saved (4 sequences, 2048 shared, 8 kv heads) 14.8 and 11.3 us, 96 MB 22.7 and
-  // 19.4, 120 MB (16 sequences, 2048 shared) 22.8 and 21.8, 240 MB (16 sequences,
-  // 1024 shared, 32 kv heads) 32.3 and 38.6, 448 MB 27.7 and 50.9.
-  const long long saved = (batch - 1ll) * prefix_len * c->n_kv_heads * c->head_dim * 4;
-  p.prefix = saved >= (128ll << 20) ? prefix_len : 0;
+  // more than that pass costs; else every sequence reads it (from the pages of
+  // row 0 all the same).  Saved are the batch - 1 further readings: from L2, at 12
+  // TB/s for heads of 128 and 10 for 64, or from memory where the prefix does not
+  // stay in L2.  The pass costs about 6 us, 1.1 for each step of 128 keys that a
+  // share takes, and 2 ns for each sequence and head, whose parts are joined.
+  // (us with the pass and without: 8 sequences, 4096 shared and 100 of their own,
+  // 32/8 heads of 128: 21.0, 19.8, with 50 of their own 18.0, 19.4; 16, 2048: 17.8,
+  // 20.8; 2, 8192, 32/32: 52.2, 34.9; 64, 512, 32/8: 27.3, 25.4; 32, 8192, 14/2 of
+  // 64: 17.6, 22.3.  Over 220 batches of 2 to 128 sequences with 16 to 2000 MB of
+  // further readings the slower way costs 12.6% at most, 0.3% on average; with a
+  // limit of 128 MB instead, 49% and 1.5%.)
+  if (batch > 1 && prefix_len > 0) {
+    p.tokens = serq::attn::kTileRows / p.group;
+    const long long items = (long long)(batch + 2 * p.tokens - 1) / (2 * p.tokens) * c->n_kv_heads;
+    p.pshares = serq::attn::tc_shares(items, prefix_len, sm_count());
+    const double once = (double)prefix_len * c->n_kv_heads * c->head_dim * 4;
+    const double per_us = once > 100e6 ? 6.4e6 : c->head_dim == 128 ? 12e6 : 10e6;
+    const double steps = (double)items * prefix_len / serq::attn::kTileKeys / p.pshares;
+    if (once * (batch - 1) / per_us > 6.0 + 1.1 * steps + 0.002 * batch * n_heads) {
+      p.prefix = prefix_len;
+      p.plonger = items * prefix_len > 2048ll * p.pshares;
+      p.pslots = 2 * (size_t)p.pshares + items;
+    }
+  }
   const long long cap = (long long)max_pages * c->page_size;
   const long long keys = std::max(0ll, (max_kv ? std::min<long long>(max_kv, cap) : cap) - p.prefix);
   const long long blocks = (keys + serq::attn::kBlockKeys - 1) / serq::attn::kBlockKeys * batch * c->n_kv_heads * p.row_blocks;
@@ -2186,14 +2203,7 @@ DecodePlan decode_plan(const serq_kv_cache* c, int batch, int n_heads, int max_p
   // with two, 13.8 with one and 12.5 with four; 600 keys 8.8, 8.2 and 11.1
   p.shares = (int)std::max(1ll, std::min<long long>((blocks + 1) / 2, 2 * sm_count()));
   p.slots = 2 * (size_t)p.shares;
-  if (p.prefix) {
-    p.slots += (size_t)batch * c->n_kv_heads * p.row_blocks;
-    p.tokens = serq::attn::kTileRows / p.group;
-    const long long items = (long long)(batch + 2 * p.tokens - 1) / (2 * p.tokens) * c->n_kv_heads;
-    p.pshares = serq::attn::tc_shares(items, p.prefix, sm_count());
-    p.plonger = items * p.prefix > 2048ll * p.pshares;
-    p.pslots = 2 * (size_t)p.pshares + items;
-  }
+  if (p.prefix) p.slots += (size_t)batch * c->n_kv_heads * p.row_blocks;
   p.ws = (p.slots * p.rows + p.pslots * 256) * (c->head_dim + 1) * sizeof(float);
   return p;
 }
