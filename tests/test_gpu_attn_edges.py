@@ -269,3 +269,20 @@ def test_tables_wider_than_the_sequences(S, q_lens, past, Hq, Hkv, D, page):
             o = S.attn_decode(cache, qd.cuda(), i32(kv), i32(wide), max_kv=hint)
             check(o, dref, dtol, dwritten, Hq, D)
     assert S.device_error() == 0
+
+
+def test_one_sequence_a_little_above_one_item_per_sm(S):
+    """One chunk whose tile pairs are a few more than the SMs, over a long
+    context: their number is exact, and a second round for a few is not taken."""
+    rng = np.random.default_rng(109)
+    T, kv, Hq, Hkv, D, page = 301, 2600, 128, 1, 64, 64   # 151 pairs of two tokens
+    table, n_pages = make_table(rng, [kv], page)
+    cache, k, v = make_cache(S, rng, [kv], table, n_pages, Hkv, page, D)
+    ws = S.attn_prefill_ws(cache, T, Hq, 1, table.shape[1])
+    assert ws is not None
+    ws.view(torch.float32).fill_(float("nan"))
+    q = bf(rng.normal(size=(T, Hq * D)))
+    o = S.attn_prefill(cache, q.cuda(), i32([0, T]), i32([kv]), i32(table), ws=ws)
+    ref, tol, written = A.attention(f64(q).reshape(T, Hq, D), k, v, [0, T], [kv], table)
+    check(o, ref, tol, written, Hq, D)
+    assert S.device_error() == 0

@@ -2088,8 +2088,8 @@ PrefillPlan prefill_plan(const serq_kv_cache* c, int T, int n_heads, int batch, 
   p.pairs = std::min(T / pair + std::min(batch, T), (T + batch * (pair - 1)) / pair);
   const long long cap = (long long)max_pages * c->page_size, items = p.pairs * c->n_kv_heads, sms = sm_count();
   const long long keys = max_kv ? std::min<long long>(max_kv, cap) : cap;
-  // (items is a bound: a little above one per SM it may well be one)
-  const long long rounds = items * 7 < sms * 8 ? 1 : 2, saved = keys * (rounds * sms - items) / (128 * sms);
+  // (several sequences: items is a bound, a little above one per SM it may well be one)
+  const long long rounds = items <= sms || (batch > 1 && items * 7 < sms * 8) ? 1 : 2, saved = keys * (rounds * sms - items) / (128 * sms);
   const bool share = items < 2 * sms && saved >= 5 + items / 16 && (rounds == 1 || keys * batch >= 3ll * T);
   p.shares = share ? serq::attn::tc_shares(items, keys, (int)sms) : 0;
   p.longer = keys > 2048;
