@@ -50,7 +50,7 @@ struct TcArgs {
   float* plse;  // and log2 of their sums [slot][row of the pair], -inf: nothing
   float c;           // |scale| log2 e, never 0
   int neg;           // scale < 0: the product is taken with -Q
-  int T, n_heads, group, tokens;  // tokens: per tile, 128 / group
+  int T, group, tokens;  // tokens: per tile, 128 / group
   int pair_shift;    // log2 of a pair's tokens, or -1
   int shares;        // > 0: equal shares of the work for that many CTAs; 0: whole items
   int prefix;        // > 0: decode rows; every row is at sequence 0's first `prefix` keys, up to its own kv_len

@@ -24,7 +24,7 @@ namespace serq {
 // kv_len[b] - 1; position p of the sequence lives in page
 // table[b * ldt + p / page_size].
 struct BatchArgs {
-  const int32_t* cu_q;    // batch + 1, nullptr: one row per sequence
+  const int32_t* cu_q;    // batch + 1; nullptr in decode, whose row b is sequence b's
   const int32_t* kv_len;  // batch
   const int32_t* table;   // batch rows of max_pages entries
   int batch, max_pages, ldt;
@@ -43,7 +43,6 @@ __device__ __forceinline__ void note_bad_page() { atomicCAS(&g_device_status, 0,
 // (the whole warp calls).  batch when t lies in front of the first or behind
 // the last one.
 __device__ __forceinline__ int warp_find_seq(const BatchArgs& b, int t, int lane) {
-  if (b.cu_q == nullptr) return t;
   int n = 0;
   for (int i = lane; i < b.batch; i += 32) n += b.cu_q[i + 1] <= t;
   n = __reduce_add_sync(0xffffffffu, n);
@@ -182,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) k_rope_append(const Args a) {
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss += x0[j] * x0[j] + x1[j] * x1[j];
-        const uint32_t mask = (TPH == 32 ? 0xffffffffu : ((1u << TPH) - 1u) << (lane & ~(TPH - 1)));
+        const uint32_t mask = ((1u << TPH) - 1u) << (lane & ~(TPH - 1));
 #pragma unroll
         for (int m = TPH / 2; m; m >>= 1) ss += __shfl_xor_sync(mask, ss, m);
         const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);

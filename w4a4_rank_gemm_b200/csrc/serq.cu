@@ -2137,7 +2137,6 @@ serq_status serq_attn_prefill(const serq_kv_cache* cache, const void* Q, int ldq
   a.c = attn_scale(scale);
   a.neg = scale < 0.f;
   a.T = T;
-  a.n_heads = n_heads;
   a.group = p.group;
   a.tokens = p.tokens;
   a.pair_shift = pair_shift(p.tokens);
@@ -2270,7 +2269,6 @@ serq_status serq_attn_decode(const serq_kv_cache* cache, const void* Q, int ldq,
     a.c = d.c;
     a.neg = scale < 0.f;
     a.T = batch;
-    a.n_heads = n_heads;
     a.group = p.group;
     a.tokens = p.tokens;
     a.pair_shift = pair_shift(p.tokens);
