@@ -640,7 +640,10 @@ serq_status serq_mx_linear(const serq_mx_layer* q, const void* Xq, const void* x
  * max_pages, is not followed: such a token is not stored, its key and value
  * count as zeros in attention (positions past the table are left out), and
  * serq_device_error reports 5.
- * Cached keys and values of positions below kv_len[b] have to be finite; what
+ * Cached keys and values of positions below kv_len[b] have to be finite, values
+ * at most 2^63 in magnitude and scores scale log2(e) q . k finite in fp32 (a
+ * step's weights sum to at most 2^40 before the division, and a row has at most
+ * 2^24 steps of 128 keys: O stays finite in fp32 while it is summed); what
  * lies behind them in a page, and other pages, may hold anything.  A NaN in a
  * query, or in a key or value that a row sees, gives that row results that are
  * not finite (one in a value also rows of the sequence in front of it), never

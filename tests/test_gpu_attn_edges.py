@@ -286,3 +286,27 @@ def test_one_sequence_a_little_above_one_item_per_sm(S):
     ref, tol, written = A.attention(f64(q).reshape(T, Hq, D), k, v, [0, T], [kv], table)
     check(o, ref, tol, written, Hq, D)
     assert S.device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_values(S, D):
+    """Values up to 2^63, with scores that rise so that weights are large while
+    a row is summed."""
+    rng = np.random.default_rng(108)
+    page, kv, rows = 64, 3000, 140
+    table, n_pages = make_table(rng, [kv], page)
+    cache, k, v = make_cache(S, rng, [kv], table, n_pages, 1, page, D)
+    for j in range(kv):
+        k[table[0, j // page], 0, j % page] = 0.0
+        k[table[0, j // page], 0, j % page, 0] = 22.0 * (j >= 128) + rng.uniform(0, 0.1)
+    kt, vt = bf(k), bf(np.nan_to_num(v) * 2.0 ** 60)
+    cache.K.copy_(kt), cache.V.copy_(vt)
+    q = np.zeros((rows, 1, D), np.float32)
+    q[:, :, 0] = 1.0
+    ref, tol, written = A.attention(q.astype(np.float64), f64(kt), f64(vt), [0, rows], [kv], table, scale=1.0)
+    for hint in (0, 1):
+        o = S.attn_prefill(cache, bf(q.reshape(rows, -1)).cuda(), i32([0, rows]), i32([kv]), i32(table), scale=1.0,
+                           max_kv=hint)
+        check(o, ref, tol, written, 1, D)
+    o = S.attn_decode(cache, bf(q[-1]).cuda(), i32([kv]), i32(table), scale=1.0)
+    check(o, ref[-1:], tol[-1:], written[-1:], 1, D)
