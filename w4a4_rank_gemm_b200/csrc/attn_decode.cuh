@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           l0 += (e[0][0] + e[0][1]) + (e[1][0] + e[1][1]);
           l1 += (e[0][2] + e[0][3]) + (e[1][2] + e[1][3]);
           // The weights are rounded to bf16, the type of V that the product wants:
-          // an error of 2^-9 on average in each, so that the result's, rounded to
+          // an error of at most 2^-8 in each, so that the result's, rounded to
           // bf16 anyway, is 2.2e-3 where it would be 1.66e-3 (root mean square,
           // 8191 keys).  A second product with what the rounding leaves over brings
           // that back for 0 to 1% where memory bounds the call, and 3 to 9% in

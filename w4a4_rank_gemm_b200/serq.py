@@ -811,8 +811,9 @@ def attn_prefill(cache: KVCache, Q: torch.Tensor, cu_q: torch.Tensor, kv_len: to
                  max_kv: int = 0, stream=None) -> torch.Tensor:
     """serq_attn_prefill: causal attention of the packed rows Q (T x heads *
     head_dim) over their sequences' cached keys; scale defaults to
-    1 / sqrt(head_dim), ws to scratch allocated here.  Rows outside the batch
-    are left as they are in O."""
+    1 / sqrt(head_dim), ws to scratch allocated here.  max_kv, a bound on the
+    lengths, chooses the work's split: give it where the table is wider than the
+    sequences are long.  Rows outside the batch are left as they are in O."""
     T, n_heads, ldq = _token_rows(Q, "Q", cache)
     if cu_q is None:
         raise ValueError("cu_q is needed")
