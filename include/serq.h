@@ -616,8 +616,8 @@ serq_status serq_mx_linear(const serq_mx_layer* q, const void* Xq, const void* x
  *
  * Rows of Q, K, V and O are token rows as the linears write them: bf16, head
  * h in columns [h D, (h + 1) D), row stride a multiple of 8 elements.  D =
- * head_dim is 64 or 128.  n_heads is a multiple of the cache's n_kv_heads
- * with n_heads / n_kv_heads <= 128; query head h reads kv head
+ * head_dim is 64 or 128.  n_heads <= 65535 is a multiple of the cache's
+ * n_kv_heads with n_heads / n_kv_heads <= 128; query head h reads kv head
  * h / (n_heads / n_kv_heads).
  *
  * The batch (all DEVICE int32, read when the kernels run, so a captured call
@@ -702,7 +702,7 @@ void serq_rope_destroy(serq_rope* rope); /* NULL accepted */
  *               element e at p page_stride + (h page_size + s) head_dim + e.
  *  n_pages      >= 1
  *  page_size    16, 32, 64, 128 or 256 tokens
- *  n_kv_heads   >= 1, n_kv_heads page_size < 2^31
+ *  n_kv_heads   1 ... 65535
  *  head_dim     64 or 128
  *  page_stride  elements, >= n_kv_heads page_size head_dim, a multiple of 8
  *               (more than that where layers share a page's memory); times 2

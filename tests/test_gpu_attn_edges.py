@@ -310,3 +310,11 @@ def test_large_values(S, D):
         check(o, ref, tol, written, 1, D)
     o = S.attn_decode(cache, bf(q[-1]).cuda(), i32([kv]), i32(table), scale=1.0)
     check(o, ref[-1:], tol[-1:], written[-1:], 1, D)
+
+
+def test_a_cache_has_pages(S):
+    with pytest.raises(ValueError, match="at least one page"):
+        S.KVCache(0, 64, 2, 128)
+    K = torch.empty((1, 65536, 16, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(S.SerqError):
+        S.KVCache(K=K, V=K)

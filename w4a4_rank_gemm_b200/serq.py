@@ -654,8 +654,8 @@ class KVCache:
             K = torch.empty(shape, dtype=torch.bfloat16, device=device or "cuda")
             V = torch.empty_like(K)
         for t, n in ((K, "K"), (V, "V")):
-            if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 4 or not t[0].is_contiguous():
-                raise ValueError(f"{n} must be a 4-D bf16 CUDA tensor, dense within a page")
+            if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape[0] < 1 or not t[0].is_contiguous():
+                raise ValueError(f"{n} must be a 4-D bf16 CUDA tensor of at least one page, dense within a page")
         if K.shape != V.shape or K.device != V.device or (K.shape[0] > 1 and K.stride(0) != V.stride(0)):
             raise ValueError("K and V must have one shape, device and page stride")
         self.K, self.V = K, V
