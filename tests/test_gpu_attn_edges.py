@@ -318,3 +318,46 @@ def test_a_cache_has_pages(S):
     K = torch.empty((1, 65536, 16, 64), dtype=torch.bfloat16, device="cuda")
     with pytest.raises(S.SerqError):
         S.KVCache(K=K, V=K)
+
+
+def test_workspace_shared_by_two_graphs_replayed_in_turn(S):
+    """Two captured calls with one workspace, replayed in turn on one stream,
+    with work that is cut and joined in both; the results are those of eager
+    calls with workspaces of their own."""
+    rng = np.random.default_rng(110)
+    Hq, Hkv, D, page = 8, 2, 128, 64
+    jobs = []
+    for kv in ([3000, 400], [900, 2048]):
+        table, n_pages = make_table(rng, kv, page)
+        cache, k, v = make_cache(S, rng, kv, table, n_pages, Hkv, page, D)
+        q = bf(rng.normal(size=(2, Hq * D))).cuda()
+        jobs.append([cache, q, i32(kv), i32(table), i32([0, 1, 2])])
+
+    def needs(j):
+        cols = j[3].shape[1]
+        return (S._ws_bytes(j[0], S.lib.serq_attn_prefill_ws_bytes, 2, Hq, 2, cols, 0),
+                S._ws_bytes(j[0], S.lib.serq_attn_decode_ws_bytes, 2, Hq, cols, 0, 0))
+
+    n = max(max(needs(j)) for j in jobs)
+    assert min(min(needs(j)) for j in jobs) > 0
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # NaN as floats
+    want, graphs, outs = [], [], []
+    for cache, q, lens, tab, cu in jobs:
+        want.append((S.attn_prefill(cache, q, cu, lens, tab), S.attn_decode(cache, q, lens, tab)))
+        o = [torch.empty_like(q) for _ in range(2)]
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            S.attn_prefill(cache, q, cu, lens, tab, O=o[0], ws=ws)
+            S.attn_decode(cache, q, lens, tab, O=o[1], ws=ws)
+        graphs.append(g)
+        outs.append(o)
+    for _ in range(10):
+        for o in outs:
+            o[0].fill_(7.0), o[1].fill_(7.0)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for (a, b), o in zip(want, outs):
+            assert torch.equal(a, o[0]) and torch.equal(b, o[1])
+    assert S.device_error() == 0
