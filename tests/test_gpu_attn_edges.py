@@ -361,3 +361,25 @@ def test_workspace_shared_by_two_graphs_replayed_in_turn(S):
         for (a, b), o in zip(want, outs):
             assert torch.equal(a, o[0]) and torch.equal(b, o[1])
     assert S.device_error() == 0
+
+
+def test_items_longer_than_a_second(S):
+    """A tile whose next item waits for the other tile's, which lasts longer
+    than the waits' second."""
+    rng = np.random.default_rng(111)
+    D, page, far, H, n = 128, 256, 3 << 25, 150, 200   # two rounds of items; the first of one row, a tile's
+    K, V = (bf(rng.normal(size=(2, H, page, D))).cuda() for _ in range(2))
+    cache = S.KVCache(K=K, V=V)
+    table = torch.zeros((2, far // page), dtype=torch.int32, device="cuda")
+    table[1] = 1
+    q = bf(rng.normal(size=(1 + n, H * D)))
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    torch.cuda.synchronize()
+    e0.record()
+    o = S.attn_prefill(cache, q.cuda(), i32([0, 1, 1 + n]), i32([far, n]), table, max_kv=1)
+    e1.record()
+    torch.cuda.synchronize()
+    assert e0.elapsed_time(e1) > 2200.0, "two items last less than the waits' limit: nothing is tested"
+    assert S.device_error() == 0
+    ref, tol, written = A.attention(f64(q[1:]).reshape(n, H, D), f64(K), f64(V), [0, n], [n], np.array([[1]]))
+    check(o[1:], ref, tol, written, H, D)

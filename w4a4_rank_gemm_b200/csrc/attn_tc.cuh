@@ -48,6 +48,10 @@ static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= kTcThreads * 168, "regist
 constexpr int kFmaPairs = 4;  // of 16 pairs of exponentials, how many go to the FMA pipe
 constexpr float kSumLimit = 1.0995116e12f;  // 2^40: see LONG below
 constexpr float kLazyMax = 8.0f;            // log2: how far a row's scores may exceed the maximum in use
+// Limit of the waits that may last as long as an item or the kernel: for a work
+// item, and a tile's for its scores while the other tile's item goes on (an item
+// of 80 million keys lasts a second).
+constexpr unsigned long long kItemWaitNs = 100 * kWaitLimitNs;
 
 struct TcArgs {
   __nv_bfloat16* o;
@@ -727,7 +731,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (uint32_t n = 0;; ++n) {
         // lasts as long as the kernel does: the MMA thread, whose own waits are
         // bounded, always ends it
-        if (!__all_sync(0xffffffffu, mbar_wait_idle(clean_ask, n & 1, abort_flag, kDevTimeoutMma, 100 * kWaitLimitNs))) break;
+        if (!__all_sync(0xffffffffu, mbar_wait_idle(clean_ask, n & 1, abort_flag, kDevTimeoutMma, kItemWaitNs))) break;
         const int vs = clean_req[0], have = clean_req[1];
         __syncwarp();
         if (vs < 0) break;
@@ -762,7 +766,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           ranked_item(a, mine, i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x), lane, it);
         }
         if (!__all_sync(0xffffffffu, mbar_wait_idle(&it_empty[i & 1], ((i >> 1) & 1) ^ 1, abort_flag,
-                                                    kDevTimeoutProducer, 100 * kWaitLimitNs)))
+                                                    kDevTimeoutProducer, kItemWaitNs)))
           break;
         if (lane == 0) {
           item_at(i) = it;
@@ -782,7 +786,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int tok = row / a.group, head = row - tok * a.group;
     uint32_t sn = 0, on = 0;
     for (int i = 0;; ++i) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&it_full[i & 1], (i >> 1) & 1, abort_flag, kDevTimeoutEpilogue))) break;
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(&it_full[i & 1], (i >> 1) & 1, abort_flag, kDevTimeoutEpilogue, kItemWaitNs)))
+        break;
       const Item it = item_at(i);
       __syncwarp();
       if (lane == 0) mbar_arrive(&it_empty[i & 1]);
@@ -798,7 +804,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float mc = -INFINITY, l = 0.f;
       bool ok = true;
       for (int j = it.j0; j < end; ++j) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], sn++ & 1, abort_flag, kDevTimeoutEpilogue));
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], sn++ & 1, abort_flag, kDevTimeoutEpilogue, kItemWaitNs));
         if (!ok) break;
         tc_fence_after();
         // The scores are read from TMEM twice, for the maximum and for the
